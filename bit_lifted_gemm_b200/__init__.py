@@ -9,11 +9,14 @@ no fallback: if liblq.so is missing or cannot be loaded, import fails loudly.
 Entry points (same names as include/lq.h, minus the `lq_` prefix):
     lifted_dim, pack_signs, unpack_signs, lift_activations,
     lift_activations_kron, gemv_workspace_size, gemv, lift_gemv, gemm, encode,
-    get_device_status (lq_selftest_wait_timeout is reached through `lib`)
+    gemm_epilogue, gemv_epilogue, gemm_grouped, group_rows, combine_rows (and the
+    workspace sizes of the first three), get_device_status
+    (lq_selftest_wait_timeout is reached through `lib`)
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -25,11 +28,14 @@ LIB_PATH = os.path.join(_HERE, "liblq_debug.so" if DEBUG else "liblq.so")
 LQ_OK, LQ_ERR_INVALID_ARG, LQ_ERR_UNSUPPORTED, LQ_ERR_CUDA, LQ_ERR_TIMEOUT, LQ_ERR_TOO_LARGE = 0, 1, 2, 3, 4, 5
 LQ_ERR_BOUNDS = 6
 LQ_F32, LQ_BF16 = 0, 1
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # lq_act
 GEMV_NOALLOC_SCRATCH_BYTES = 4 << 20  # LQ_GEMV_NOALLOC_SCRATCH_BYTES of include/lq.h
 
 SYMBOLS = ("lq_status_str", "lq_lifted_dim", "lq_pack_signs", "lq_unpack_signs", "lq_lift_activations",
            "lq_lift_activations_kron", "lq_gemv_workspace_size", "lq_gemv", "lq_gemv_noalloc", "lq_lift_gemv",
-           "lq_gemm", "lq_encode", "lq_selftest_wait_timeout", "lq_selftest_bounds", "lq_is_debug_build",
+           "lq_gemm", "lq_gemm_epilogue", "lq_gemm_epilogue_workspace_size", "lq_gemv_epilogue",
+           "lq_gemv_epilogue_workspace_size", "lq_gemm_grouped", "lq_gemm_grouped_workspace_size",
+           "lq_group_rows", "lq_combine_rows", "lq_encode", "lq_selftest_wait_timeout", "lq_selftest_bounds", "lq_is_debug_build",
            "lq_get_device_status")
 
 
@@ -76,6 +82,17 @@ def _load() -> ctypes.CDLL:
     lib.lq_is_debug_build.argtypes = []
     lib.lq_encode.argtypes = [p, i, i, p, i, i, p, i, p, p]
     lib.lq_gemm.argtypes = [p, p, i, i, p, i, p, p]
+    for name, argtypes in (("lq_gemm_epilogue_workspace_size", [i, i, i]), ("lq_gemv_epilogue_workspace_size", [i, i, i]),
+                           ("lq_gemm_grouped_workspace_size", [i, i, i, i])):
+        getattr(lib, name).restype = z
+        getattr(lib, name).argtypes = argtypes
+    layer = [p, p, i, i, p, i, p, i, i, p, p, i, p, z, p]
+    for name, argtypes in (("lq_gemm_epilogue", layer), ("lq_gemv_epilogue", layer),
+                           ("lq_gemm_grouped", [p, p, i, i, i, p, i, p, p, i, p, i, i, p, i, p, z, p]),
+                           ("lq_group_rows", [p, i, i, i, p, p, p, p]),
+                           ("lq_combine_rows", [p, i, i, i, p, p, i, i, p, p, p])):
+        getattr(lib, name).restype = i
+        getattr(lib, name).argtypes = argtypes
     lib.lq_get_device_status.restype = i
     lib.lq_get_device_status.argtypes = [p]
     return lib
@@ -284,6 +301,195 @@ def encode(w, M, K, err=False, out=None, stream=None):
     e = torch.empty((rows, in_dim // d), dtype=torch.float32, device=w.device) if err else None
     _check(lib.lq_encode(_ptr(w), rows, in_dim, _ptr(M), d, D, _ptr(out), K, _ptr(e), _stream(stream)), "lq_encode")
     return (out, e) if err else out
+
+
+# ------------------------------------------------------------------ fused epilogues and grouped products
+
+def _on(t, stream):
+    """Context in which `t`'s device is current, with `stream` (if given) as the
+    current stream, so that what a call allocates belongs to the stream it runs on."""
+    import torch
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _operand(t, name, dtype, shape, device):
+    """Checks one operand of the calls below (None passes): contiguous, on `device`, of this type and shape."""
+    if t is None:
+        return
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.device != device or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _float_type(o_dtype, name="o_dtype"):
+    import torch
+    if o_dtype in ("f32", torch.float32):
+        return torch.float32, LQ_F32
+    if o_dtype in ("bf16", torch.bfloat16):
+        return torch.bfloat16, LQ_BF16
+    raise ValueError(f"{name} must be 'f32' or 'bf16'")
+
+
+def _activation(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(k for k in ACTIVATIONS if k)} or None")
+    return ACTIVATIONS[act]
+
+
+def gemm_epilogue_workspace_size(out_rows: int, K: int, tokens: int) -> int:
+    """Bytes of workspace gemm_epilogue needs (0: refused sizes)."""
+    return int(lib.lq_gemm_epilogue_workspace_size(out_rows, K, tokens))
+
+
+def gemv_epilogue_workspace_size(out_rows: int, K: int, batch: int) -> int:
+    """Bytes of workspace gemv_epilogue needs (0: refused sizes)."""
+    return int(lib.lq_gemv_epilogue_workspace_size(out_rows, K, batch))
+
+
+def gemm_grouped_workspace_size(experts: int, out_rows: int, K: int, n: int) -> int:
+    """Bytes of workspace gemm_grouped needs (0: refused sizes)."""
+    return int(lib.lq_gemm_grouped_workspace_size(experts, out_rows, K, n))
+
+
+def _scratch(ws, need, device):
+    import torch
+    if ws is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)  # 512-byte aligned
+    _dev_tensor(ws, "workspace")
+    if ws.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return ws
+
+
+def _layer_epilogue(fn, size_fn, u_type, packed, s, u, bias, act, glu, residual, o_dtype, out, workspace, stream):
+    import torch
+    if u.dim() != 2 or packed.dim() != 2:
+        raise ValueError("packed must be [out][K/32] and u [tokens][K]")
+    tokens, K = u.shape
+    rows, dev = packed.shape[0], u.device
+    ot, o_t = _float_type(o_dtype if out is None else out.dtype)
+    width = rows // 2 if glu else rows
+    with _on(u, stream):
+        if out is None:
+            out = torch.empty((tokens, width), dtype=ot, device=dev)
+        for t, name, dtype, shape in ((u, "u", u_type, (tokens, K)), (packed, "packed", torch.int32, (rows, K // 32)),
+                                      (s, "s", torch.float32, (rows,)), (bias, "bias", torch.float32, (rows,)),
+                                      (residual, "residual", ot, (tokens, width)), (out, "out", ot, (tokens, width))):
+            _operand(t, name, dtype, shape, dev)
+        ws = _scratch(workspace, size_fn(rows, K, tokens), dev)
+        _check(getattr(lib, fn)(_ptr(packed), _ptr(s), rows, K, _ptr(u), tokens, _ptr(bias), _activation(act),
+                                int(bool(glu)), _ptr(residual), _ptr(out), o_t, _ptr(ws),
+                                ws.numel() * ws.element_size(), _stream(stream)), fn)
+    return out
+
+
+def gemm_epilogue(packed, s, u, bias=None, act=None, glu=False, residual=None, o_dtype="f32", out=None,
+                  workspace=None, stream=None):
+    """packed [out][K/32], s [out], u bf16 [tokens][K] -> o [tokens][width], o_dtype "f32" or "bf16".
+
+    z = s * (W_q u) + bias; o = act(z) + residual with width = out, or with glu
+    (rows 2i the gate's, rows 2i+1 the other factor's) o[i] = act(z[2i]) * z[2i+1] +
+    residual[i] with width = out/2. act: None, "relu", "gelu", "gelu_tanh" or "silu";
+    bias fp32 [out]; residual in o's type. `workspace` (gemm_epilogue_workspace_size
+    bytes) is allocated when not given; calls that share one must be ordered."""
+    import torch
+    return _layer_epilogue("lq_gemm_epilogue", gemm_epilogue_workspace_size, torch.bfloat16, packed, s, u, bias, act,
+                           glu, residual, o_dtype, out, workspace, stream)
+
+
+def gemv_epilogue(packed, s, u, bias=None, act=None, glu=False, residual=None, o_dtype="f32", out=None,
+                  workspace=None, stream=None):
+    """gemm_epilogue for decode: u fp32 [batch][K], batch <= 16, at fp32 accuracy."""
+    import torch
+    return _layer_epilogue("lq_gemv_epilogue", gemv_epilogue_workspace_size, torch.float32, packed, s, u, bias, act,
+                           glu, residual, o_dtype, out, workspace, stream)
+
+
+def gemm_grouped(packed, s, u, offsets, n, rows=None, bias=None, act=None, glu=False, o_dtype="f32", out=None,
+                 workspace=None, stream=None):
+    """Products grouped by expert: packed [experts][out][K/32], s [experts][out], u bf16 [tokens][K],
+    offsets int32 [experts+1], rows int32 [n] or None -> o [n][width].
+
+    Slot i of expert e (offsets[e] <= i < offsets[e+1]) takes row rows[i] of u (row i
+    without rows) through expert e's layer and the epilogue of gemm_epilogue (bias fp32
+    [experts][out]). offsets and rows, as group_rows gives them, stay on the device.
+    Slots of no expert are not written: uninitialized when `out` is allocated here."""
+    import torch
+    if u.dim() != 2 or packed.dim() != 3:
+        raise ValueError("packed must be [experts][out][K/32] and u [tokens][K]")
+    tokens, K = u.shape
+    experts, out_rows = packed.shape[:2]
+    n, dev = int(n), u.device
+    ot, o_t = _float_type(o_dtype if out is None else out.dtype)
+    width = out_rows // 2 if glu else out_rows
+    with _on(u, stream):
+        if out is None:
+            out = torch.empty((n, width), dtype=ot, device=dev)
+        for t, name, dtype, shape in ((u, "u", torch.bfloat16, (tokens, K)),
+                                      (packed, "packed", torch.int32, (experts, out_rows, K // 32)),
+                                      (s, "s", torch.float32, (experts, out_rows)),
+                                      (offsets, "offsets", torch.int32, (experts + 1,)),
+                                      (rows, "rows", torch.int32, (n,)),
+                                      (bias, "bias", torch.float32, (experts, out_rows)),
+                                      (out, "out", ot, (n, width))):
+            _operand(t, name, dtype, shape, dev)
+        ws = _scratch(workspace, gemm_grouped_workspace_size(experts, out_rows, K, n), dev)
+        _check(lib.lq_gemm_grouped(_ptr(packed), _ptr(s), experts, out_rows, K, _ptr(u), tokens, _ptr(rows),
+                                   _ptr(offsets), n, _ptr(bias), _activation(act), int(bool(glu)), _ptr(out), o_t,
+                                   _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "lq_gemm_grouped")
+    return out
+
+
+def group_rows(expert_ids, experts, offsets=None, rows=None, slots=None, stream=None):
+    """Router choices int32 [tokens][topk] -> (offsets int32 [experts+1], rows int32 [tokens*topk],
+    slots int32 [tokens][topk]): expert e's slots are [offsets[e], offsets[e+1]) in (token, choice)
+    order, rows the token of each slot (-1 past the last), slots the slot of each choice (-1 for
+    ids outside 0..experts-1)."""
+    import torch
+    if expert_ids.dim() != 2:
+        raise ValueError("expert_ids must be [tokens][topk]")
+    tokens, topk = expert_ids.shape
+    dev = expert_ids.device
+    with _on(expert_ids, stream):
+        new = lambda t, shape: torch.empty(shape, dtype=torch.int32, device=dev) if t is None else t  # noqa: E731
+        offsets, rows, slots = new(offsets, (experts + 1,)), new(rows, (tokens * topk,)), new(slots, (tokens, topk))
+        for t, name, shape in ((expert_ids, "expert_ids", (tokens, topk)), (offsets, "offsets", (experts + 1,)),
+                               (rows, "rows", (tokens * topk,)), (slots, "slots", (tokens, topk))):
+            _operand(t, name, torch.int32, shape, dev)
+        _check(lib.lq_group_rows(_ptr(expert_ids), tokens, topk, experts, _ptr(offsets), _ptr(rows), _ptr(slots),
+                                 _stream(stream)), "lq_group_rows")
+    return offsets, rows, slots
+
+
+def combine_rows(y, slots, weights, residual=None, out=None, stream=None):
+    """o[t] = residual[t] + sum_j weights[t][j] * y[slots[t][j]]: y [n][width] (float32 or bfloat16), slots
+    int32 [tokens][topk] (values outside 0..n-1 add nothing), weights fp32 [tokens][topk], residual and o
+    [tokens][width] in y's type."""
+    import torch
+    if y.dim() != 2 or slots.dim() != 2:
+        raise ValueError("y must be [n][width] and slots [tokens][topk]")
+    n, width = y.shape
+    tokens, topk = slots.shape
+    dev = y.device
+    yt, y_t = _float_type(y.dtype, "y's type")
+    with _on(y, stream):
+        if out is None:
+            out = torch.empty((tokens, width), dtype=yt, device=dev)
+        for t, name, dtype, shape in ((y, "y", yt, (n, width)), (slots, "slots", torch.int32, (tokens, topk)),
+                                      (weights, "weights", torch.float32, (tokens, topk)),
+                                      (residual, "residual", yt, (tokens, width)), (out, "out", yt, (tokens, width))):
+            _operand(t, name, dtype, shape, dev)
+        _check(lib.lq_combine_rows(_ptr(y), y_t, n, width, _ptr(slots), _ptr(weights), tokens, topk, _ptr(residual),
+                                   _ptr(out), _stream(stream)), "lq_combine_rows")
+    return out
 
 
 def get_device_status(stream=None) -> int:

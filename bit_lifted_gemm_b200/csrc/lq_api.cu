@@ -111,6 +111,29 @@ bool aliased(std::initializer_list<Span> spans) {
 
 size_t nbytes(long long count, size_t elem) { return (size_t)count * elem; }
 
+// True if every non-null pointer is device memory of the current device, or
+// managed memory.
+bool all_on_current_device(std::initializer_list<const void*> ps) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    for (const void* p : ps) {
+        if (!p) continue;
+        cudaPointerAttributes at;
+        if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        if (at.type != cudaMemoryTypeManaged && (at.type != cudaMemoryTypeDevice || at.device != dev)) return false;
+    }
+    return true;
+}
+
+bool all_aligned16(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (!aligned16(p)) return false;
+    return true;
+}
+
 // Device address of the status word on the current device (looked up once per device).
 unsigned* status_word(int* err) {
     static unsigned* addr[kMaxDevices] = {};
@@ -377,6 +400,162 @@ int lq_gemm(const uint32_t* packed, const float* s, int out, int K, const uint16
     return from_cuda(lq::launch_gemm(packed, s, out, K, u_bf16, tokens, o, status, static_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- fused epilogues and grouped products
+
+}  // extern "C"
+
+namespace {
+
+// The checks and the launch that lq_gemm_epilogue, lq_gemv_epilogue and
+// lq_gemm_grouped share; c.n, c.tokens, c.experts and c.out are positive and K
+// is a valid lifted width.
+int grouped_call(const lq::GroupedCall& c, int o_dtype, int glu, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    if (!c.packed || !c.s || !c.u || !c.o || !workspace) return LQ_ERR_INVALID_ARG;
+    if (!all_aligned16({c.packed, c.s, c.u, c.rows, c.offsets, c.bias, c.residual, c.o})) return LQ_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LQ_ERR_INVALID_ARG;
+    if (o_dtype != LQ_F32 && o_dtype != LQ_BF16) return LQ_ERR_INVALID_ARG;
+    if (c.act < LQ_ACT_NONE || c.act > LQ_ACT_SILU || (glu != 0 && glu != 1)) return LQ_ERR_INVALID_ARG;
+    if (glu && c.out % 2 != 0) return LQ_ERR_INVALID_ARG;
+    const size_t need = lq::grouped_workspace_size(c);
+    if (workspace_bytes < need) return LQ_ERR_INVALID_ARG;
+    const long long rows_w = (long long)c.experts * c.out, width = glu ? c.out / 2 : c.out;
+    const size_t oe = c.o_bf16 ? 2 : 4;
+    if (aliased({{c.packed, nbytes(rows_w * (c.K / 32), 4), false},
+                 {c.s, nbytes(rows_w, 4), false},
+                 {c.u, nbytes((long long)c.tokens * c.K, c.u_bf16 ? 2 : 4), false},
+                 {c.rows, nbytes(c.n, 4), false},
+                 {c.offsets, nbytes(c.experts + 1, 4), false},
+                 {c.bias, nbytes(rows_w, 4), false},
+                 {c.residual, nbytes(c.n * width, oe), false},
+                 {c.o, nbytes(c.n * width, oe), true},
+                 {workspace, need, true}}))
+        return LQ_ERR_INVALID_ARG;
+    if (fault_is("launch")) return LQ_ERR_CUDA;
+    const int sm = is_sm100();
+    if (sm < 0) return LQ_ERR_CUDA;
+    if (sm == 0) return LQ_ERR_UNSUPPORTED;
+    if (!all_on_current_device({c.packed, c.s, c.u, c.rows, c.offsets, c.bias, c.residual, c.o, workspace}))
+        return LQ_ERR_INVALID_ARG;
+    int err = LQ_OK;
+    unsigned* status = status_word(&err);
+    if (!status) return err;
+    return from_cuda(lq::launch_grouped(c, workspace, status, static_cast<cudaStream_t>(stream)));
+}
+
+// A call of one layer on all its rows.
+lq::GroupedCall layer_call(const uint32_t* packed, const float* s, int out, int K, const void* u, bool u_bf16,
+                           int tokens, const float* bias, int act, int glu, const void* residual, void* o,
+                           int o_dtype) {
+    return lq::GroupedCall{packed, s,    1,   out,      K,        u, u_bf16, tokens, nullptr, nullptr, tokens,
+                           bias,   act, glu != 0, residual, o, o_dtype == LQ_BF16};
+}
+
+bool layer_sizes_ok(int out, int K) { return out >= 1 && K >= 32 && K % 32 == 0; }
+
+constexpr int kMaxExperts = 4096;
+
+bool grouped_sizes_ok(int experts, int out, int K, int n) {
+    return layer_sizes_ok(out, K) && experts >= 1 && experts <= kMaxExperts && n >= 1 &&
+           (long long)experts * out <= 0x7fffffffLL;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lq_gemm_epilogue_workspace_size(int out, int K, int tokens) {
+    if (!layer_sizes_ok(out, K) || tokens < 1) return 0;
+    return lq::grouped_workspace_size(
+        layer_call(nullptr, nullptr, out, K, nullptr, true, tokens, nullptr, 0, 0, nullptr, nullptr, LQ_F32));
+}
+
+int lq_gemm_epilogue(const uint32_t* packed, const float* s, int out, int K, const uint16_t* u_bf16, int tokens,
+                     const float* bias, int act, int glu, const void* residual, void* o, int o_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    if (!layer_sizes_ok(out, K) || tokens < 1) return LQ_ERR_INVALID_ARG;
+    return grouped_call(layer_call(packed, s, out, K, u_bf16, true, tokens, bias, act, glu, residual, o, o_dtype),
+                        o_dtype, glu, workspace, workspace_bytes, stream);
+}
+
+size_t lq_gemv_epilogue_workspace_size(int out, int K, int batch) {
+    if (!layer_sizes_ok(out, K) || batch < 1 || batch > 16) return 0;
+    return lq::grouped_workspace_size(
+        layer_call(nullptr, nullptr, out, K, nullptr, false, batch, nullptr, 0, 0, nullptr, nullptr, LQ_F32));
+}
+
+int lq_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K, const float* u, int batch,
+                     const float* bias, int act, int glu, const void* residual, void* o, int o_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    if (!layer_sizes_ok(out, K) || batch < 1 || batch > 16) return LQ_ERR_INVALID_ARG;
+    return grouped_call(layer_call(packed, s, out, K, u, false, batch, bias, act, glu, residual, o, o_dtype), o_dtype,
+                        glu, workspace, workspace_bytes, stream);
+}
+
+size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n) {
+    if (!grouped_sizes_ok(experts, out, K, n)) return 0;
+    lq::GroupedCall c =
+        layer_call(nullptr, nullptr, out, K, nullptr, true, n, nullptr, 0, 0, nullptr, nullptr, LQ_F32);
+    c.experts = experts;
+    return lq::grouped_workspace_size(c);
+}
+
+int lq_gemm_grouped(const uint32_t* packed, const float* s, int experts, int out, int K, const uint16_t* u_bf16,
+                    int tokens, const int* rows, const int* offsets, int n, const float* bias, int act, int glu,
+                    void* o, int o_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!grouped_sizes_ok(experts, out, K, n) || tokens < 1 || !offsets) return LQ_ERR_INVALID_ARG;
+    if (!rows && tokens < n) return LQ_ERR_INVALID_ARG;
+    lq::GroupedCall c = layer_call(packed, s, out, K, u_bf16, true, tokens, bias, act, glu, nullptr, o, o_dtype);
+    c.experts = experts;
+    c.rows = rows;
+    c.offsets = offsets;
+    c.n = n;
+    return grouped_call(c, o_dtype, glu, workspace, workspace_bytes, stream);
+}
+
+int lq_group_rows(const int* expert_ids, int tokens, int topk, int experts, int* offsets, int* rows, int* slots,
+                  void* stream) {
+    if (!expert_ids || !offsets || !rows || !slots || !all_aligned16({expert_ids, offsets, rows, slots}))
+        return LQ_ERR_INVALID_ARG;
+    if (tokens < 1 || topk < 1 || experts < 1 || experts > kMaxExperts || (long long)tokens * topk > 0x7fffffffLL)
+        return LQ_ERR_INVALID_ARG;
+    const size_t each = nbytes((long long)tokens * topk, 4);
+    if (aliased({{expert_ids, each, false},
+                 {offsets, nbytes(experts + 1, 4), true},
+                 {rows, each, true},
+                 {slots, each, true}}))
+        return LQ_ERR_INVALID_ARG;
+    if (fault_is("launch")) return LQ_ERR_CUDA;
+    const int sm = is_sm100();
+    if (sm < 0) return LQ_ERR_CUDA;
+    if (sm == 0) return LQ_ERR_UNSUPPORTED;
+    if (!all_on_current_device({expert_ids, offsets, rows, slots})) return LQ_ERR_INVALID_ARG;
+    return from_cuda(lq::launch_group_rows(expert_ids, tokens, topk, experts, offsets, rows, slots,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int lq_combine_rows(const void* y, int dtype, int n, int width, const int* slots, const float* weights, int tokens,
+                    int topk, const void* residual, void* o, void* stream) {
+    if (!y || !slots || !weights || !o || !all_aligned16({y, slots, weights, residual, o})) return LQ_ERR_INVALID_ARG;
+    if (dtype != LQ_F32 && dtype != LQ_BF16) return LQ_ERR_INVALID_ARG;
+    if (n < 1 || width < 1 || tokens < 1 || topk < 1 || (long long)tokens * topk > 0x7fffffffLL)
+        return LQ_ERR_INVALID_ARG;
+    const size_t e = dtype == LQ_BF16 ? 2 : 4;
+    if (aliased({{y, nbytes((long long)n * width, e), false},
+                 {slots, nbytes((long long)tokens * topk, 4), false},
+                 {weights, nbytes((long long)tokens * topk, 4), false},
+                 {residual, nbytes((long long)tokens * width, e), false},
+                 {o, nbytes((long long)tokens * width, e), true}}))
+        return LQ_ERR_INVALID_ARG;
+    if (fault_is("launch")) return LQ_ERR_CUDA;
+    const int sm = is_sm100();
+    if (sm < 0) return LQ_ERR_CUDA;
+    if (sm == 0) return LQ_ERR_UNSUPPORTED;
+    if (!all_on_current_device({y, slots, weights, residual, o})) return LQ_ERR_INVALID_ARG;
+    return from_cuda(lq::launch_combine_rows(y, dtype == LQ_BF16, n, width, slots, weights, tokens, topk, residual, o,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
 int lq_get_device_status(void* stream) {
     if (fault_is("timeout")) return LQ_ERR_TIMEOUT;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -395,7 +574,7 @@ int lq_get_device_status(void* stream) {
     // every file's flag is read and cleared, whichever is set
     const unsigned bounds = lq::debug_take_gemm() | lq::debug_take_lift() | lq::debug_take_lift_kron() |
                             lq::debug_take_lift_tc() | lq::debug_take_lift_kron_tc() | lq::debug_take_encode() |
-                            lq::debug_take_pack() | lq::debug_take_selftest();
+                            lq::debug_take_pack() | lq::debug_take_rows() | lq::debug_take_selftest();
     if (bounds) return LQ_ERR_BOUNDS;
 #endif
     return (v & LQ_DEV_TIMEOUT) ? LQ_ERR_TIMEOUT : LQ_OK;

@@ -65,6 +65,7 @@ unsigned debug_take_lift_tc();
 unsigned debug_take_lift_kron_tc();
 unsigned debug_take_encode();
 unsigned debug_take_pack();
+unsigned debug_take_rows();
 unsigned debug_take_selftest();
 #endif
 
@@ -101,5 +102,33 @@ cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodeP
 cudaError_t launch_gemm(const uint32_t* packed, const float* s, int out, int K,
                         const uint16_t* u_bf16, int tokens, float* o, unsigned* status,
                         cudaStream_t st);
+
+// One call of the grouped product with its epilogue (lq_grouped.cu). A layer
+// without experts is the case experts = 1, offsets = NULL (all n slots).
+struct GroupedCall {
+    const uint32_t* packed;  // [experts][out][K/32]
+    const float* s;          // [experts][out]
+    int experts, out, K;
+    const void* u;  // [tokens][K], fp32 (at most 16 slots, one expert) or bf16
+    bool u_bf16;
+    int tokens;          // rows of u
+    const int* rows;     // [n] row of u of each slot, or NULL: slot i takes row i
+    const int* offsets;  // [experts + 1] on the device, or NULL
+    int n;               // slots
+    const float* bias;   // [experts][out] or NULL
+    int act;
+    bool glu;
+    const void* residual;  // [n][width] in o's type, or NULL
+    void* o;               // [n][width], width = glu ? out / 2 : out
+    bool o_bf16;
+};
+size_t grouped_workspace_size(const GroupedCall& c);  // sizes and types of c alone
+cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st);
+
+// Rows grouped by expert id, and the experts' rows joined per token (lq_rows.cu).
+cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts, int* offsets, int* rows, int* slots,
+                              cudaStream_t st);
+cudaError_t launch_combine_rows(const void* y, bool bf16, int n, int width, const int* slots, const float* weights,
+                                int tokens, int topk, const void* residual, void* o, cudaStream_t st);
 
 }  // namespace lq

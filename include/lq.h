@@ -277,6 +277,109 @@ LQ_API int lq_gemv_noalloc(const uint32_t* packed, const float* s, int out, int 
 LQ_API int lq_gemm(const uint32_t* packed, const float* s, int out, int K,
             const uint16_t* u_bf16, int tokens, float* o, void* stream);
 
+/* Activations of the fused epilogues below, fp32 in and out:
+ *   NONE z; RELU max(z, 0); GELU z/2 (1 + erf(z/sqrt 2));
+ *   GELU_TANH z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); SILU z / (1 + e^-z). */
+typedef enum {
+    LQ_ACT_NONE = 0,
+    LQ_ACT_RELU = 1,
+    LQ_ACT_GELU = 2,
+    LQ_ACT_GELU_TANH = 3,
+    LQ_ACT_SILU = 4
+} lq_act;
+
+/* The 1-bit product with bias, activation (or gate) and residual in its
+ * epilogue, for bf16 u and any number of tokens (a single one included):
+ *   z[t][r] = s[r] * sum_k sigma[r][k] * u[t][k] + bias[r]
+ *   glu = 0: o[t][r] = act(z[t][r]) + residual[t][r]            width = out
+ *   glu = 1: o[t][i] = act(z[t][2i]) * z[t][2i+1] + residual[t][i]  width = out/2
+ *            (rows 2i are the gate's, rows 2i+1 the other factor's; out even)
+ *   packed   : uint32 [out][K/32]; s : fp32 [out]; u_bf16 : bf16 [tokens][K]
+ *   bias     : fp32 [out] or NULL
+ *   act      : an lq_act; glu 0 or 1
+ *   residual : [tokens][width] in o's type, or NULL
+ *   o        : [tokens][width], o_dtype LQ_F32 or LQ_BF16 (written)
+ *   workspace: 256-byte aligned device memory of at least
+ *              lq_gemm_epilogue_workspace_size(out, K, tokens) bytes; its contents
+ *              before the call do not matter. Calls that share one must be ordered.
+ *   out >= 1, K >= 32, K % 32 == 0, tokens >= 1
+ * Products are exact, sums are fp32, and the result is rounded once, to o's type.
+ * A NaN or Inf in a row of u reaches that row of o alone. Every pointer must be
+ * memory of the current device. Requires an sm_100 device (else
+ * LQ_ERR_UNSUPPORTED). */
+LQ_API int lq_gemm_epilogue(const uint32_t* packed, const float* s, int out, int K,
+                            const uint16_t* u_bf16, int tokens, const float* bias, int act, int glu,
+                            const void* residual, void* o, int o_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace lq_gemm_epilogue needs; 0 for sizes it refuses. Host only. */
+LQ_API size_t lq_gemm_epilogue_workspace_size(int out, int K, int tokens);
+
+/* The same epilogue for decode with fp32 u [batch][K], batch 1..16, at fp32
+ * accuracy (no rounding of u to 16 bits). Arguments as lq_gemm_epilogue;
+ * workspace of lq_gemv_epilogue_workspace_size(out, K, batch) bytes. */
+LQ_API int lq_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K,
+                            const float* u, int batch, const float* bias, int act, int glu,
+                            const void* residual, void* o, int o_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace lq_gemv_epilogue needs; 0 for sizes it refuses. Host only. */
+LQ_API size_t lq_gemv_epilogue_workspace_size(int out, int K, int batch);
+
+/* Products grouped by expert with ragged sizes: expert e's layer is applied to
+ * the slots offsets[e] <= i < offsets[e+1],
+ *   z[i][r] = s[e][r] * sum_k sigma[e][r][k] * u[rows[i]][k] + bias[e][r]
+ * followed by act or the gate as in lq_gemm_epilogue (no residual).
+ *   packed  : uint32 [experts][out][K/32]; s : fp32 [experts][out]
+ *   u_bf16  : bf16 [tokens][K]; rows : int32 [n], the row of u that slot i takes,
+ *             or NULL for row i. A slot whose row is outside 0..tokens-1 is
+ *             computed as if its row of u were zero; nothing is read for it.
+ *   offsets : int32 [experts+1] in device memory (read by the kernels only, so
+ *             the call needs no synchronization and can be captured in a graph).
+ *             Ascending in 0..n; values outside are taken as the nearest allowed
+ *             ones. Experts may be empty; sizes may differ freely.
+ *   n       : slots, the extent of rows and o
+ *   bias    : fp32 [experts][out] or NULL
+ *   o       : [n][width], o_dtype; only slots of some expert are written
+ *   workspace: lq_gemm_grouped_workspace_size(experts, out, K, n) bytes, as above
+ *   experts 1..4096, experts*out below 2^31, tokens >= 1, n >= 1
+ * A slot's result does not depend on which other slots are in the call's groups
+ * beyond fp32 rounding. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
+LQ_API int lq_gemm_grouped(const uint32_t* packed, const float* s, int experts, int out, int K,
+                           const uint16_t* u_bf16, int tokens, const int* rows, const int* offsets, int n,
+                           const float* bias, int act, int glu, void* o, int o_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace lq_gemm_grouped needs; 0 for sizes it refuses. Host only. */
+LQ_API size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n);
+
+/* Groups the (token, choice) pairs of a router by expert, for lq_gemm_grouped:
+ *   expert_ids : int32 [tokens][topk]; ids outside 0..experts-1 are left out (a
+ *                dropped choice, or an expert that lives elsewhere)
+ *   offsets    : int32 [experts+1] (written): expert e has slots
+ *                [offsets[e], offsets[e+1]); offsets[experts] pairs are kept
+ *   rows       : int32 [tokens*topk] (written): the token of each slot, -1 from
+ *                offsets[experts] on
+ *   slots      : int32 [tokens][topk] (written): the slot of each pair, -1 if left out
+ * Within an expert slots follow (token, choice) order, so the result is unique.
+ * tokens >= 1, topk >= 1, tokens*topk below 2^31, experts 1..4096; int32 arrays 16-byte
+ * aligned like every tensor. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
+LQ_API int lq_group_rows(const int* expert_ids, int tokens, int topk, int experts, int* offsets,
+                         int* rows, int* slots, void* stream);
+
+/* Joins the experts' rows per token:
+ *   o[t] = residual[t] + sum_j weights[t][j] * y[slots[t][j]]
+ * summed in fp32 in the order of j (the residual last) and rounded once.
+ *   y        : [n][width], dtype LQ_F32 or LQ_BF16
+ *   slots    : int32 [tokens][topk]; values outside 0..n-1 add nothing
+ *   weights  : fp32 [tokens][topk]
+ *   residual : [tokens][width] of the same dtype, or NULL
+ *   o        : [tokens][width] of the same dtype (written); a token with no slot
+ *              gets its residual, or zeros
+ * n, width, tokens, topk >= 1. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
+LQ_API int lq_combine_rows(const void* y, int dtype, int n, int width, const int* slots, const float* weights,
+                           int tokens, int topk, const void* residual, void* o, void* stream);
+
 /* Self-test of the failure reporting: launches one thread that waits, through
  * the bounded-wait helper the GEMV and GEMM use, on an mbarrier that nothing
  * ever completes. After limit_us microseconds (1 .. 1000000) the wait gives up,

@@ -1,0 +1,139 @@
+"""Host-side checks of the fused-epilogue, grouped and row operators, without a GPU: bad arguments are refused
+before any CUDA call, outputs may not overlap other buffers, workspace sizes, and the plain forms' own pins."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from tests import operators_plain as plain
+
+BIG = 1 << 40
+
+
+def far(i):
+    """Distinct fake addresses, 64 GiB apart, never dereferenced."""
+    return ctypes.c_void_p((i + 1) << 36)
+
+
+MIS = ctypes.c_void_p((1 << 36) + 4)
+
+LAYER = dict(packed=far(0), s=far(1), out=8, K=64, u=far(2), tokens=4, bias=far(3), act=4, glu=1, residual=far(4), o=far(5),
+             o_dtype=1, workspace=far(6), bytes=BIG, stream=None)
+GROUPED = dict(packed=far(0), s=far(1), experts=3, out=8, K=64, u=far(2), tokens=4, rows=far(3), offsets=far(4), n=8,
+               bias=far(5), act=4, glu=1, o=far(6), o_dtype=0, workspace=far(7), bytes=BIG, stream=None)
+GROUP = dict(ids=far(0), tokens=4, topk=2, experts=8, offsets=far(1), rows=far(2), slots=far(3), stream=None)
+COMBINE = dict(y=far(0), dtype=1, n=8, width=16, slots=far(1), weights=far(2), tokens=4, topk=2, residual=far(3), o=far(4),
+               stream=None)
+BASE = {"lq_gemm_epilogue": LAYER, "lq_gemv_epilogue": LAYER, "lq_gemm_grouped": GROUPED, "lq_group_rows": GROUP,
+        "lq_combine_rows": COMBINE}
+
+BAD = [(fn, {key: None}) for fn, base in BASE.items() for key, v in base.items()
+       if isinstance(v, ctypes.c_void_p) and (key not in ("bias", "residual", "rows") or fn == "lq_group_rows")]
+BAD += [(fn, {key: MIS}) for fn, base in BASE.items() for key, v in base.items() if isinstance(v, ctypes.c_void_p)]
+for fn in ("lq_gemm_epilogue", "lq_gemv_epilogue", "lq_gemm_grouped"):
+    BAD += [(fn, c) for c in ({"out": 0}, {"out": 7}, {"K": 0}, {"K": 48}, {"K": -32}, {"tokens": 0}, {"act": -1}, {"act": 5}, {"glu": 2},
+                              {"glu": -1}, {"o_dtype": 2}, {"bytes": 0}, {"workspace": ctypes.c_void_p((7 << 36) + 16)})]
+BAD += [("lq_gemv_epilogue", {"tokens": 17}), ("lq_gemm_grouped", {"experts": 0}), ("lq_gemm_grouped", {"experts": 4097}),
+        ("lq_gemm_grouped", {"n": 0}), ("lq_gemm_grouped", {"experts": 4096, "out": 1 << 20}),
+        ("lq_gemm_grouped", {"rows": None, "n": 5}), ("lq_group_rows", {"tokens": 0}), ("lq_group_rows", {"topk": 0}),
+        ("lq_group_rows", {"experts": 0}), ("lq_group_rows", {"experts": 4097}),
+        ("lq_group_rows", {"tokens": 1 << 20, "topk": 1 << 12}), ("lq_combine_rows", {"dtype": 2}), ("lq_combine_rows", {"n": 0}),
+        ("lq_combine_rows", {"width": 0}), ("lq_combine_rows", {"tokens": 0}), ("lq_combine_rows", {"topk": 0}),
+        ("lq_combine_rows", {"tokens": 1 << 20, "topk": 1 << 12})]
+
+
+def call(fn, **change):
+    import bit_lifted_gemm_b200 as lq
+    return getattr(lq.lib, fn)(*{**BASE[fn], **change}.values())
+
+
+@pytest.mark.parametrize("fn,change", BAD, ids=lambda v: v if isinstance(v, str) else "-".join(f"{k}={x}" for k, x in v.items()))
+def test_bad_arguments_refused(fn, change, monkeypatch):
+    import bit_lifted_gemm_b200 as lq
+    monkeypatch.setenv("LQ_FAULT", "launch")  # what is accepted by mistake launches nothing
+    assert call(fn, **change) == lq.LQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fn", list(BASE))
+def test_good_arguments_pass_the_checks(fn, monkeypatch):
+    import bit_lifted_gemm_b200 as lq
+    monkeypatch.setenv("LQ_FAULT", "launch")
+    assert call(fn) == lq.LQ_ERR_CUDA
+    optional = [k for k in ("bias", "residual", "rows") if k in BASE[fn] and fn != "lq_group_rows"]
+    change = {k: None for k in optional}
+    if fn == "lq_gemm_grouped":
+        change["tokens"] = 8
+    assert call(fn, **change) == lq.LQ_ERR_CUDA
+
+
+@pytest.mark.parametrize("fn,outputs", [("lq_gemm_epilogue", ["o", "workspace"]), ("lq_gemv_epilogue", ["o", "workspace"]),
+                                        ("lq_gemm_grouped", ["o", "workspace"]),
+                                        ("lq_group_rows", ["offsets", "rows", "slots"]), ("lq_combine_rows", ["o"])])
+def test_outputs_may_not_overlap(fn, outputs, monkeypatch):
+    import bit_lifted_gemm_b200 as lq
+    monkeypatch.setenv("LQ_FAULT", "launch")
+    for o in outputs:
+        for key, v in BASE[fn].items():
+            if isinstance(v, ctypes.c_void_p) and key != o:
+                assert call(fn, **{o: v}) == lq.LQ_ERR_INVALID_ARG, (o, key)
+
+
+def test_inputs_may_overlap(monkeypatch):
+    import bit_lifted_gemm_b200 as lq
+    monkeypatch.setenv("LQ_FAULT", "launch")
+    assert call("lq_gemm_epilogue", bias=far(1)) == lq.LQ_ERR_CUDA
+    assert call("lq_combine_rows", residual=far(0)) == lq.LQ_ERR_CUDA
+
+
+def test_workspace_sizes():
+    import bit_lifted_gemm_b200 as lq
+    assert lq.gemm_epilogue_workspace_size(13824, 12288, 2048) >= 1
+    assert lq.gemv_epilogue_workspace_size(13824, 12288, 16) >= 1
+    assert lq.gemm_grouped_workspace_size(8, 4096, 10240, 8192) >= 1
+    assert lq.gemm_epilogue_workspace_size(8, 48, 1) == 0
+    assert lq.gemm_epilogue_workspace_size(0, 64, 1) == 0
+    assert lq.gemv_epilogue_workspace_size(8, 64, 17) == 0
+    assert lq.gemm_grouped_workspace_size(4097, 8, 64, 1) == 0
+    assert lq.gemm_grouped_workspace_size(4, 8, 64, 0) == 0
+    need = lq.gemv_epilogue_workspace_size(300, 1536, 5)
+    import os
+    os.environ["LQ_FAULT"] = "launch"
+    try:
+        big = dict(out=300, K=1536, tokens=5)
+        assert call("lq_gemv_epilogue", bytes=need, **big) == lq.LQ_ERR_CUDA
+        assert call("lq_gemv_epilogue", bytes=need - 1, **big) == lq.LQ_ERR_INVALID_ARG
+    finally:
+        del os.environ["LQ_FAULT"]
+
+
+def test_plain_layer_against_hand_values():
+    packed = np.array([[0b101], [0xFFFFFFFF]], np.uint32)
+    u = np.zeros((1, 32))
+    u[0, :3] = 1, 2, 4
+    z = plain.layer(packed, np.array([2.0, 1.0]), u)[0]
+    assert z.tolist() == [[2 * (1 - 2 + 4), 7.0]]
+    assert plain.layer(packed, np.array([2.0, 1.0]), u, glu=True, bias=np.array([1.0, -1.0]))[0].tolist() == [[7.0 * 6.0]]
+
+
+def test_plain_group_and_combine_against_hand_values():
+    offsets, rows, slots = plain.group(np.array([[1, 0], [1, -1], [0, 5]]), 2)
+    assert offsets.tolist() == [0, 2, 4] and rows.tolist() == [0, 2, 0, 1, -1, -1]
+    assert slots.tolist() == [[2, 0], [3, -1], [1, -1]]
+    y = np.arange(8.0).reshape(4, 2)
+    o, _ = plain.combine(y, slots, np.full((3, 2), 0.5))
+    assert o.tolist() == [[0.5 * 4 + 0, 0.5 * 5 + 0.5], [3.0, 3.5], [1.0, 1.5]]
+
+
+def test_experts_block_checks_its_widths():
+    import torch
+    from bit_lifted_gemm_b200.experts import ExpertMLP, interleave_rows
+    gate, up = torch.zeros((2, 8, 3), dtype=torch.int32), torch.ones((2, 8, 3), dtype=torch.int32)
+    both = interleave_rows(gate, up)
+    assert both.shape == (2, 16, 3) and both[0, :, 0].tolist() == [0, 1] * 8
+    with pytest.raises(ValueError):
+        interleave_rows(gate, up[:, :4])
+    M = torch.zeros((10, 24))
+    s = torch.zeros((2, 16))
+    with pytest.raises(ValueError):  # model = 40 channels lift to 96 columns = 3 words, hidden = 8 is no multiple of d
+        ExpertMLP(both, s, torch.zeros((2, 40, 1), dtype=torch.int32), s, M)
