@@ -59,11 +59,17 @@ __global__ void __launch_bounds__(32 * kWarps) grouped_kernel(const GroupedCall 
 
 }  // namespace
 
-size_t grouped_workspace_size(const GroupedCall&) { return 256; }
+size_t grouped_workspace_size(const GroupedCall& c) {
+    const size_t planes = grouped_mma_workspace_size(c.K, c.n, c.u_bf16);
+    return planes > 256 ? planes : 256;
+}
 
 cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st) {
-    (void)ws;
-    (void)status;
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int active = c.n < c.experts ? c.n : c.experts;
+    if (!c.u_bf16 || (c.n + active - 1) / active <= 32) return launch_grouped_mma(c, ws, status, st, sms);
     const int width = c.glu ? c.out / 2 : c.out;
     const dim3 grid((width + kWarps - 1) / kWarps, c.n < 16384 ? c.n : 16384);
     grouped_kernel<<<grid, 32 * kWarps, 0, st>>>(c);
