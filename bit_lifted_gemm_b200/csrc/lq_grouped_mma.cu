@@ -30,6 +30,7 @@
 // words are rotated by 16 to match.
 #include "lq_debug.cuh"
 #include "lq_epilogue.cuh"
+#include "lq_grouped.cuh"
 #include "lq_internal.h"
 #include "lq_sm100.cuh"
 
@@ -79,63 +80,26 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     return v;
 }
 
-// Bits j and j + 16 of w as a pair of bf16 +-1.
-__device__ __forceinline__ uint32_t sign_pair(uint32_t w, int j) {
-    return ((w << (15 - j)) & 0x80008000u) ^ 0xBF80BF80u;
-}
-
 struct Plan {
+    uint32_t shift[16];  // 2^(15 - j): kept from the compiler, so that it multiplies (see sign_pair)
     int stages, stage_bytes, cols_cap, cols_pass, nblk;
     int planes;  // columns per slot: 1, or 3 bf16 parts of an fp32 u
     size_t smem;
 };
 
-// Walks the units (expert, block of rows, pass of columns) in order; passes of one
-// block are neighbours, so that the weights a second pass reads are still in L2.
-struct UnitWalk {
-    long long before = 0;  // units before expert e0
-    int e0 = 0;            // first expert of the current window of 32
-
-    // Unit `unit`, if there is one (warp-collective): expert, first slot, slots, first weight row.
-    __device__ bool find(const GroupedCall& c, const Plan& p, long long unit, int lane, int& e, int& slot0, int& slots,
-                         int& row0) {
-        const int per = p.cols_pass / p.planes;  // slots of a pass
-        while (e0 < c.experts) {
-            const int mine = e0 + lane;
-            int lo = 0, hi = 0;
-            if (mine < c.experts) {
-                lo = c.offsets ? min(max(__ldg(c.offsets + mine), 0), c.n) : 0;
-                hi = c.offsets ? max(min(__ldg(c.offsets + mine + 1), c.n), lo) : c.n;
-            }
-            const long long units = (long long)((hi - lo + per - 1) / per) * p.nblk;
-            long long upto = units;
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long x = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += x;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, before + upto > unit);
-            if (past) {
-                const int src = __ffs(past) - 1;
-                const long long rest = unit - before - __shfl_sync(0xffffffffu, upto - units, src);
-                lo = __shfl_sync(0xffffffffu, lo, src);
-                hi = __shfl_sync(0xffffffffu, hi, src);
-                const int npass = (hi - lo + per - 1) / per;
-                const int blk = (int)(rest / npass), pass = (int)(rest - (long long)blk * npass);
-                e = e0 + src;
-                slot0 = lo + pass * per;
-                slots = min(per, hi - slot0);
-                row0 = blk;
-                return true;
-            }
-            before += __shfl_sync(0xffffffffu, upto, 31);
-            e0 += 32;
-        }
-        return false;
-    }
-};
+// Bits j and j + 16 of w as a pair of bf16 +-1. The shift is written as a product
+// with a kernel argument: an integer multiply-add runs on the FMA pipe beside the
+// logic operation on the ALU pipe, and the ALU pipe (half a warp instruction per
+// clock) bounded the kernel with both on it.
+__device__ __forceinline__ uint32_t sign_pair(uint32_t w, const Plan& p, int j) {
+    const uint32_t x = j == 15 ? w : w * p.shift[j];
+    uint32_t r;  // (x & b) ^ c in one instruction
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "r"(0x80008000u), "r"(0xBF80BF80u));
+    return r;
+}
 
 template <int H, int NT, int VEC>
-__global__ void __launch_bounds__(kThreads, 1) mma_kernel(const GroupedCall c, const Plan p, unsigned* status) {
+__global__ void __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant__ GroupedCall c, const __grid_constant__ Plan p, unsigned* status) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int R = 16 * H, RP = R + 4, COLS = 8 * NT;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
@@ -157,13 +121,15 @@ __global__ void __launch_bounds__(kThreads, 1) mma_kernel(const GroupedCall c, c
     __syncthreads();
 
     UnitWalk walk;
-    int e, slot0, slots, blk, st = 0, phase = 0;
+    Unit u;
+    const int per = p.cols_pass / p.planes;  // slots of a unit
+    int st = 0, phase = 0;
     if (warp >= kConsumers) {
         // ---- producers
         const int tid = threadIdx.x - 32 * kConsumers;
         bool stop = false;  // the same in all lanes of a warp
-        for (long long unit = blockIdx.x; !stop && walk.find(c, p, unit, lane, e, slot0, slots, blk); unit += gridDim.x) {
-            const int row0 = blk * R, cols = slots * p.planes;
+        for (long long unit = blockIdx.x; !stop && walk.find<true>(c, per, p.nblk, unit, lane, u); unit += gridDim.x) {
+            const int e = u.e, slot0 = u.slot0, slots = u.slots, row0 = u.blk * R, cols = slots * p.planes;
             const uint32_t* w0 = c.packed + ((long long)e * c.out + row0) * kw;
             const int rows_left = c.out - row0;
             for (int run = 0; run < runs; ++run) {
@@ -212,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_kernel(const GroupedCall c, c
     const int g = lane >> 2, t = lane & 3, quarter = warp & 3, group = warp >> 2;
     const uint32_t rot = t >= 2 ? 0x1032u : 0x3210u;
     long long done = 0;  // runs before this unit, over all units
-    for (long long unit = blockIdx.x; walk.find(c, p, unit, lane, e, slot0, slots, blk); unit += gridDim.x) {
-        const int row0 = blk * R, cols = slots * p.planes;
+    for (long long unit = blockIdx.x; walk.find<true>(c, per, p.nblk, unit, lane, u); unit += gridDim.x) {
+        const int e = u.e, slot0 = u.slot0, slots = u.slots, row0 = u.blk * R, cols = slots * p.planes;
         float acc[H][NT][4];
 #pragma unroll
         for (int i = 0; i < H; ++i)
@@ -260,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_kernel(const GroupedCall c, c
                         const uint32_t wl = __byte_perm(lds32(at), 0, rot), wh = __byte_perm(lds32(at + 1024), 0, rot);
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const uint32_t a0 = sign_pair(wl, j), a1 = sign_pair(wh, j);
-                            const uint32_t a2 = sign_pair(wl, j + 1), a3 = sign_pair(wh, j + 1);
+                            const uint32_t a0 = sign_pair(wl, p, j), a1 = sign_pair(wh, p, j);
+                            const uint32_t a2 = sign_pair(wl, p, j + 1), a3 = sign_pair(wh, p, j + 1);
 #pragma unroll
                             for (int n = 0; n < NT; ++n) mma_bf16(acc[i][n], a0, a1, a2, a3, b[n][x][j], b[n][x][j + 1]);
                         }
@@ -367,6 +333,7 @@ cudaError_t launch_grouped_mma(const GroupedCall& call, void* ws, unsigned* stat
     GroupedCall c = call;
     Plan p{};
     p.planes = c.u_bf16 ? 1 : 3;
+    for (int j = 0; j < 16; ++j) p.shift[j] = 1u << (15 - j);
     if (!c.u_bf16) {
         const long long count = (long long)c.tokens * c.K;
         split_kernel<<<(int)((count + 255) / 256 < 4 * sms ? (count + 255) / 256 : 4 * sms), 256, 0, st>>>(

@@ -1,0 +1,363 @@
+// Products grouped by expert for many rows per expert (prefill and large batches), on
+// tcgen05; lq_grouped.cu routes here.
+//
+//   z[i][r] = s[r] sum_k sigma[r][k] u[row(i)][k] + bias[r]
+//
+// A unit is a tile of 128 weight rows by up to 256 slots of one expert; persistent
+// CTAs (one per SM) take units in turn. The MMA's width N is the tile's slots
+// rounded up to 16, so a short tail of an expert costs what it needs. K is walked in
+// steps of 64 through a ring of four stages:
+//   warp 0        u rows of the slots by TMA (128-byte swizzle): tiles of 32
+//                 consecutive rows, or four gathered rows per instruction
+//   warp 1        issues the MMAs (M = 128, K = 16, bf16, fp32 in TMEM)
+//   warps 2..9    two groups that take pairs of k-steps in turn; a thread owns one weight
+//                 row, loads its sign words well ahead and stores them as bf16 +-1 into
+//                 the stage in the swizzled layout
+//   warps 10..13  epilogue of the tile before, from the other of two accumulators:
+//                 scale, bias, activation or gate, residual, one rounding, store. A
+//                 thread owns one weight row, so a warp stores 32 neighbouring outputs.
+// Products are exact; only the fp32 sums round. Every wait is bounded.
+#include <cuda.h>
+
+#include "lq_debug.cuh"
+#include "lq_epilogue.cuh"
+#include "lq_grouped.cuh"
+#include "lq_internal.h"
+#include "lq_sm100.cuh"
+
+namespace lq {
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
+constexpr int A_STAGE = BM * BK * 2, B_STAGE = BN * BK * 2;
+constexpr int kBox = 32;  // rows of a tiled load of u
+constexpr int UNPACK_WARP = 2, EPILOGUE_WARP = 10;
+constexpr int THREADS = 32 * 14;
+constexpr size_t SMEM_BYTES = 1024 + STAGES * (A_STAGE + B_STAGE) + 256;
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Four rows of a 2-D tensor (box one row high), each 128 bytes of x.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+        : "memory");
+}
+
+// 16 sign bits (in the low half of x) as eight bf16 pairs: pair i holds bits 2i and 2i + 1.
+__device__ __forceinline__ void expand16(uint32_t x, uint32_t* v) {
+    const uint32_t q = (x & 0x5555u) | ((x & 0xAAAAu) << 15);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t y = q << (15 - 2 * i);
+        asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(v[i]) : "r"(y), "r"(0x80008000u), "r"(0xBF80BF80u));  // (y & b) ^ c
+    }
+}
+
+// One row's outputs for 32 slots of the tile, from its accumulator columns.
+__device__ __forceinline__ void store_chunk(const GroupedCall& c, const float (&z)[32], int m, int width, int slot0,
+                                            int count, int lane) {
+    const long long extent = (long long)c.n * width;
+    if (!c.glu) {
+        if (m >= c.out) return;
+        float r[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            r[j] = c.residual && j < count ? load_elem(c.residual, (long long)(slot0 + j) * width + m, c.o_bf16) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < count && LQ_IN_BOUNDS((long long)(slot0 + j) * width + m, extent)) {
+                const float y = activate(z[j], c.act);
+                store_elem(c.o, (long long)(slot0 + j) * width + m, c.o_bf16, c.residual ? y + r[j] : y);
+            }
+        return;
+    }
+    // gate rows are the even lanes', the other factors the odd lanes': lane pairs swap
+    // halves, the even lane finishes slots 0..15 and the odd lane slots 16..31
+    const bool odd = lane & 1;
+    const int j0 = odd ? 16 : 0;
+    const bool there = m < c.out;
+    float r[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        r[j] = c.residual && there && j0 + j < count
+                   ? load_elem(c.residual, (long long)(slot0 + j0 + j) * width + m / 2, c.o_bf16)
+                   : 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float own = odd ? z[16 + j] : z[j], other = __shfl_xor_sync(0xffffffffu, odd ? z[j] : z[16 + j], 1);
+        if (!there || j0 + j >= count || !LQ_IN_BOUNDS((long long)(slot0 + j0 + j) * width + m / 2, extent)) continue;
+        const float y = activate(odd ? other : own, c.act) * (odd ? own : other);
+        store_elem(c.o, (long long)(slot0 + j0 + j) * width + m / 2, c.o_bf16, c.residual ? y + r[j] : y);
+    }
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    tc_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ GroupedCall c, unsigned* status) {
+    extern __shared__ uint8_t smem_raw[];
+    // 1024-byte aligned for the 128-byte swizzle
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sA = smem_addr(smem), sB = sA + STAGES * A_STAGE;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * (A_STAGE + B_STAGE));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * STAGES;
+    const uint32_t acc_full0 = empty0 + 8 * STAGES, acc_empty0 = acc_full0 + 16, drained = acc_empty0 + 16;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kw = c.K >> 5, nkb = (c.K + BK - 1) / BK, nblk = (c.out + BM - 1) / BM;
+
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < STAGES; ++st) {
+            mbar_init(full0 + 8 * st, 1 + 128);
+            mbar_init(empty0 + 8 * st, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(acc_full0 + 8 * a, 1);
+            mbar_init(acc_empty0 + 8 * a, 128);
+        }
+        mbar_init(drained, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmap_u);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(tmem_slot), 2 * BN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // A role gives up when a wait of its own runs out or another role has given up;
+    // the decision is one for the whole warp, which walks the units together.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool ok = !*abort_flag && mbar_wait(bar, parity, status);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        *abort_flag = 1;
+        return false;
+    };
+
+    UnitWalk walk;
+    Unit u;
+    int st = 0, phase = 0;  // ring position, kept by each role
+    auto advance = [&] {
+        if (++st == STAGES) st = 0, phase ^= 1;
+    };
+    bool go = true;
+    if (warp == 0) {
+        // ---- u tiles
+        int issued = 0;
+        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+            const int boxes = (u.slots + kBox - 1) / kBox, quads = (u.slots + 15) / 16 * 4;
+            int rows[2][4] = {};
+            if (c.rows) {  // slots past the tile's and rows outside u load row 0; the epilogue leaves them out
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = 4 * (lane + 32 * h) + i;
+                        const int row = j < u.slots ? __ldg(c.rows + u.slot0 + j) : 0;
+                        rows[h][i] = row >= 0 && row < c.tokens ? row : 0;
+                    }
+            }
+            const uint32_t bytes = c.rows ? quads * 512 : boxes * kBox * 128;
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!(go = wait(empty0 + 8 * st, phase ^ 1))) break;
+                const uint32_t dst = sB + st * B_STAGE, bar = full0 + 8 * st;
+                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                __syncwarp();
+                if (c.rows) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (lane + 32 * h < quads) tma_gather4(dst + (lane + 32 * h) * 512, &tmap_u, kb * BK, rows[h], bar);
+                } else if (lane < boxes) {
+                    tma_load_2d(dst + lane * kBox * 128, &tmap_u, kb * BK, u.slot0 + lane * kBox, bar);
+                }
+                ++issued;
+                advance();
+            }
+        }
+        // leave no copy in flight: the last load of each stage has landed
+        for (int back = issued < STAGES ? issued : STAGES; back > 0; --back) {
+            const int at = issued - back;
+            mbar_wait(full0 + 8 * (at % STAGES), (at / STAGES) & 1, status);
+        }
+    } else if (warp == 1) {
+        // ---- MMAs
+        int acc = 0, acc_phase = 0;
+        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+            const uint32_t idesc = idesc_bf16_f32(BM, (u.slots + 15) / 16 * 16);
+            if (!(go = wait(acc_empty0 + 8 * acc, acc_phase ^ 1))) break;
+            tc_fence_after();
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!(go = wait(full0 + 8 * st, phase))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t a = sA + st * A_STAGE, b = sB + st * B_STAGE;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        umma_f16(tmem + acc * BN, smem_desc_sw128(a + kk * 32), smem_desc_sw128(b + kk * 32), idesc,
+                                 (kb | kk) != 0);
+                    umma_commit(empty0 + 8 * st);
+                    if (kb == nkb - 1) umma_commit(acc_full0 + 8 * acc);
+                }
+                __syncwarp();
+                advance();
+            }
+            if (++acc == 2) acc = 0, acc_phase ^= 1;
+        }
+        if (lane == 0) {  // no MMA is in flight when TMEM is freed
+            umma_commit(drained);
+            mbar_wait(drained, 0, status);
+        }
+    } else if (warp < EPILOGUE_WARP) {
+        // ---- signs: group h takes the pairs of k-steps h, h + 2, ...
+        const int group = (warp - UNPACK_WARP) >> 2, row = (threadIdx.x - 32 * UNPACK_WARP) & 127;
+        const uint32_t row_off = (row >> 3) * 1024 + (row & 7) * 128, sw = row & 7;
+        const bool vec = (kw & 3) == 0;  // rows of words 16-byte aligned
+        const int pairs = (nkb + 1) / 2;
+        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+            const int r = min(u.blk * BM + row, c.out - 1);  // rows past `out` are computed but not stored
+            const long long w0 = ((long long)u.e * c.out + r) * kw, words = (long long)c.experts * c.out * kw;
+            auto load = [&](int pair) {
+                const int x = 4 * pair;
+                uint4 v = {0, 0, 0, 0};  // u is zero past K
+                if (vec && x + 4 <= kw) {
+                    if (LQ_IN_BOUNDS(w0 + x + 3, words)) v = __ldg(reinterpret_cast<const uint4*>(c.packed + w0 + x));
+                } else if (!vec) {
+                    if (x < kw && LQ_IN_BOUNDS(w0 + x, words)) v.x = __ldg(c.packed + w0 + x);
+                    if (x + 1 < kw && LQ_IN_BOUNDS(w0 + x + 1, words)) v.y = __ldg(c.packed + w0 + x + 1);
+                    if (x + 2 < kw && LQ_IN_BOUNDS(w0 + x + 2, words)) v.z = __ldg(c.packed + w0 + x + 2);
+                    if (x + 3 < kw && LQ_IN_BOUNDS(w0 + x + 3, words)) v.w = __ldg(c.packed + w0 + x + 3);
+                }
+                return v;
+            };
+            uint4 ahead[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ahead[i] = load(group + 2 * i);
+            const int st0 = st, phase0 = phase;  // ring position of the unit's first k-step
+            for (int p0 = group; p0 < pairs && go; p0 += 8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pair = p0 + 2 * i;
+                    if (pair >= pairs || !go) break;
+                    const uint32_t w[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
+                    ahead[i] = load(pair + 8);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int kb = 2 * pair + half;
+                        if (kb >= nkb || !go) break;
+                        const int at = st0 + kb, s = at % STAGES, ph = phase0 ^ ((at / STAGES) & 1);
+                        uint32_t v[32];
+                        expand16(w[2 * half], v);
+                        expand16(w[2 * half] >> 16, v + 8);
+                        expand16(w[2 * half + 1], v + 16);
+                        expand16(w[2 * half + 1] >> 16, v + 24);
+                        if (!(go = wait(empty0 + 8 * s, ph ^ 1))) break;
+                        const uint32_t dst = sA + s * A_STAGE + row_off;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared_v4(dst + ((q ^ sw) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        fence_proxy_async_smem();
+                        mbar_arrive(full0 + 8 * s);
+                    }
+                }
+            }
+            st = st0 + nkb;
+            phase = phase0 ^ ((st / STAGES) & 1);
+            st %= STAGES;
+        }
+    } else {
+        // ---- epilogue: a warp may only reach its own quarter of the TMEM lanes (warp % 4)
+        const int q = warp & 3, width = c.glu ? c.out / 2 : c.out;
+        int acc = 0, acc_phase = 0;
+        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+            const int m = u.blk * BM + q * 32 + lane;
+            const long long at = (long long)u.e * c.out + min(m, c.out - 1);
+            const float sr = __ldg(c.s + at), br = c.bias ? __ldg(c.bias + at) : 0.f;
+            if (!(go = wait(acc_full0 + 8 * acc, acc_phase))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < u.slots; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + acc * BN + ((uint32_t)(q * 32) << 16) + c0, v);
+                unsigned there = 0xffffffffu;
+                if (c.rows) {  // a slot whose row is outside u counts as zero
+                    const int slot = u.slot0 + c0 + lane;
+                    const int row = c0 + lane < u.slots ? __ldg(c.rows + slot) : 0;
+                    there = __ballot_sync(0xffffffffu, row >= 0 && row < c.tokens);
+                }
+                tmem_ld_wait();
+                float z[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, (there >> j) & 1u ? __uint_as_float(v[j]) : 0.f, br);
+                store_chunk(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
+            }
+            tc_fence_before();
+            mbar_arrive(acc_empty0 + 8 * acc);
+            if (++acc == 2) acc = 0, acc_phase ^= 1;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<EncodeTiledFn>(p)
+                   : nullptr;
+    }();
+    return fn;
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_tc(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
+    EncodeTiledFn encode = encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    CUtensorMap map;
+    cuuint64_t gdim[2] = {(cuuint64_t)c.K, (cuuint64_t)c.tokens};
+    cuuint64_t gstride[1] = {(cuuint64_t)c.K * 2};
+    cuuint32_t box[2] = {BK, c.rows ? 1u : (cuuint32_t)kBox};
+    cuuint32_t estride[2] = {1, 1};
+    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.u), gdim, gstride, box, estride,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !attr_set[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev] = true;
+    }
+    tc_kernel<<<sms, THREADS, SMEM_BYTES, st>>>(map, c, status);
+    return cudaGetLastError();
+}
+
+}  // namespace lq
+
+LQ_DEBUG_FLAG_TAKE(debug_take_grouped_tc)
