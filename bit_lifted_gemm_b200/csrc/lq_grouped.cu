@@ -22,8 +22,9 @@ cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cud
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int active = c.n < c.experts ? c.n : c.experts;
-    if (!c.u_bf16 || (c.n + active - 1) / active <= 32) return launch_grouped_mma(c, ws, status, st, sms);
-    return launch_grouped_tc(c, status, st, sms);
+    const int each = (int)(((long long)c.n + active - 1) / active);
+    if (!c.u_bf16 || each <= 32) return launch_grouped_mma(c, ws, status, st, sms);
+    return launch_grouped_tc(c, status, st, sms, each);
 }
 
 }  // namespace lq

@@ -3,21 +3,23 @@
 //
 //   z[i][r] = s[r] sum_k sigma[r][k] u[row(i)][k] + bias[r]
 //
-// A unit is a tile of 128 weight rows by up to 256 slots of one expert; persistent
-// CTAs (one per SM) take units in turn. The MMA's width N is the tile's slots
+// A unit is a tile of 128 weight rows by up to BN slots of one expert; persistent
+// CTAs (one per SM) take units in turn (256, 128 or 64 slots to a full tile). The MMA's width N is the tile's slots
 // rounded up to 16, so a short tail of an expert costs what it needs. K is walked in
-// steps of 64 through a ring of four stages:
-//   warp 0        u rows of the slots by TMA (128-byte swizzle): tiles of 32
-//                 consecutive rows, or four gathered rows per instruction
+// steps of 64 through a ring of stages:
+//   warp 0        u rows of the slots by TMA (128-byte swizzle), without `rows`
 //   warp 1        issues the MMAs (M = 128, K = 16, bf16, fp32 in TMEM)
 //   warps 2..9    two groups that take pairs of k-steps in turn; a thread owns one weight
 //                 row, loads its sign words well ahead and stores them as bf16 +-1 into
-//                 the stage in the swizzled layout
+//                 the stage in the swizzled layout. With `rows`, the second group copies
+//                 the gathered rows of u instead, with 16-byte cp.async (TMA gathers of four rows took
+//                 75 clocks each, 4800 per k-step)
 //   warps 10..13  epilogue of the tile before, from the other of two accumulators:
 //                 scale, bias, activation or gate, residual, one rounding, store. A
 //                 thread owns one weight row, so a warp stores 32 neighbouring outputs.
 // Products are exact; only the fp32 sums round. Every wait is bounded.
 #include <cuda.h>
+#include <string.h>
 
 #include "lq_debug.cuh"
 #include "lq_epilogue.cuh"
@@ -30,24 +32,38 @@ namespace {
 
 using namespace sm100;
 
-constexpr int BM = 128, BN = 256, BK = 64, STAGES = 4;
-constexpr int A_STAGE = BM * BK * 2, B_STAGE = BN * BK * 2;
-constexpr int kBox = 32;  // rows of a tiled load of u
-constexpr int UNPACK_WARP = 2, EPILOGUE_WARP = 10;
+constexpr int BM = 128, BK = 64;
+constexpr int A_STAGE = BM * BK * 2;
+constexpr int kBox = 64;  // rows of a tiled load of u of a short tile; a long one loads all BN rows at once
+constexpr int UNPACK_WARP = 2, GATHER_WARP = 6, EPILOGUE_WARP = 10;
 constexpr int THREADS = 32 * 14;
-constexpr size_t SMEM_BYTES = 1024 + STAGES * (A_STAGE + B_STAGE) + 256;
+// A stage is freed ~400 clocks after its MMAs, refilled ~1000 later: narrow tiles need more of them in flight.
+template <int BN>
+struct Ring {
+    static constexpr int STAGES = BN == 64 ? 8 : BN == 128 ? 6 : 4;
+    static constexpr int B_STAGE = BN * BK * 2;
+    static constexpr size_t SMEM_BYTES = 1024 + STAGES * (A_STAGE + B_STAGE) + 256;
+};
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Four rows of a 2-D tensor (box one row high), each 128 bytes of x.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
-        : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {  // all but the last N groups of this thread have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One lane of a converged warp, in the form that lets the compiler keep the operands of
+// the instructions behind it in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // 16 sign bits (in the low half of x) as eight bf16 pairs: pair i holds bits 2i and 2i + 1.
@@ -98,8 +114,14 @@ __device__ __forceinline__ void store_chunk(const GroupedCall& c, const float (&
     }
 }
 
+// BN: slots of a full tile. VEC: K a multiple of 128, so that rows of sign words are
+// 16-byte aligned. GATHER: rows are given.
+template <int BN, bool VEC, bool GATHER>
 __global__ void __launch_bounds__(THREADS, 1)
-    tc_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ GroupedCall c, unsigned* status) {
+    tc_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_all,
+              const __grid_constant__ GroupedCall c, unsigned* status) {
+    constexpr int STAGES = Ring<BN>::STAGES, B_STAGE = Ring<BN>::B_STAGE;
+    constexpr int GROUPS = GATHER ? 1 : 2;  // of unpack warps
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned for the 128-byte swizzle
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -115,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < STAGES; ++st) {
-            mbar_init(full0 + 8 * st, 1 + 128);
+            mbar_init(full0 + 8 * st, GATHER ? 256 : 1 + 128);
             mbar_init(empty0 + 8 * st, 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -139,6 +161,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // A role gives up when a wait of its own runs out or another role has given up;
     // the decision is one for the whole warp, which walks the units together.
     auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         const bool ok = !*abort_flag && mbar_wait(bar, parity, status);
         if (__all_sync(0xffffffffu, ok)) return true;
         *abort_flag = 1;
@@ -152,32 +175,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++st == STAGES) st = 0, phase ^= 1;
     };
     bool go = true;
-    if (warp == 0) {
+    if (!GATHER && warp == 0) {
         // ---- u tiles
         int issued = 0;
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
-            const int boxes = (u.slots + kBox - 1) / kBox, quads = (u.slots + 15) / 16 * 4;
-            int rows[2][4] = {};
-            if (c.rows) {  // slots past the tile's and rows outside u load row 0; the epilogue leaves them out
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = 4 * (lane + 32 * h) + i;
-                        const int row = j < u.slots ? __ldg(c.rows + u.slot0 + j) : 0;
-                        rows[h][i] = row >= 0 && row < c.tokens ? row : 0;
-                    }
-            }
-            const uint32_t bytes = c.rows ? quads * 512 : boxes * kBox * 128;
+            const bool all = u.slots > BN - kBox;
+            const int boxes = all ? BN / kBox : (u.slots + kBox - 1) / kBox;
             for (int kb = 0; kb < nkb; ++kb) {
                 if (!(go = wait(empty0 + 8 * st, phase ^ 1))) break;
                 const uint32_t dst = sB + st * B_STAGE, bar = full0 + 8 * st;
-                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                if (lane == 0) mbar_arrive_expect_tx(bar, boxes * kBox * 128);
                 __syncwarp();
-                if (c.rows) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (lane + 32 * h < quads) tma_gather4(dst + (lane + 32 * h) * 512, &tmap_u, kb * BK, rows[h], bar);
+                if (all) {
+                    if (lane == 0) tma_load_2d(dst, &tmap_all, kb * BK, u.slot0, bar);
                 } else if (lane < boxes) {
                     tma_load_2d(dst + lane * kBox * 128, &tmap_u, kb * BK, u.slot0 + lane * kBox, bar);
                 }
@@ -190,27 +200,83 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int at = issued - back;
             mbar_wait(full0 + 8 * (at % STAGES), (at / STAGES) & 1, status);
         }
+    } else if (GATHER && warp >= GATHER_WARP && warp < EPILOGUE_WARP) {
+        // ---- gathered rows of u: a thread copies one 16-byte chunk of every 16th row, in the
+        // layout that a 128-byte swizzled tile has; stages are handed over LAG steps later, when they have landed
+        constexpr int LAG = STAGES - 2, ROWS = BN / 16;
+        const int tid = threadIdx.x - 32 * GATHER_WARP, chunk = tid & 7, first = tid >> 3;
+        const uint32_t off = first * 128 + ((chunk ^ (first & 7)) << 4);
+        const uint16_t* ub = static_cast<const uint16_t*>(c.u);
+        int given = 0, issued = 0;  // k-steps handed over, and begun
+        auto hand_over = [&] {
+            fence_proxy_async_smem();
+            mbar_arrive(full0 + 8 * (given % STAGES));
+            ++given;
+        };
+        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+            const int pad = (u.slots + 15) / 16;
+            int rows[ROWS];  // -1: a zero row
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                const int j = first + 16 * i;
+                const int row = j < u.slots ? __ldg(c.rows + u.slot0 + j) : -1;
+                rows[i] = row >= 0 && row < c.tokens ? row : -1;
+            }
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!(go = wait(empty0 + 8 * st, phase ^ 1))) break;
+                const uint32_t dst = sB + st * B_STAGE + off;
+                const int k = kb * BK + chunk * 8;
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i)
+                    if (i < pad) {
+                        const bool there = rows[i] >= 0 && k < c.K &&
+                                           LQ_IN_BOUNDS((long long)rows[i] * c.K + k + 7, (long long)c.tokens * c.K);
+                        cp_async16(dst + i * 2048, there ? ub + (long long)rows[i] * c.K + k : ub, there);
+                    }
+                cp_async_commit();
+                advance();
+                if (++issued > LAG) {
+                    cp_async_wait<LAG>();
+                    hand_over();
+                }
+            }
+        }
+        cp_async_wait<0>();
+        while (given < issued) hand_over();
     } else if (warp == 1) {
         // ---- MMAs
         int acc = 0, acc_phase = 0;
+        const uint64_t a_desc = smem_desc_sw128(sA), b_desc = smem_desc_sw128(sB);
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
             const uint32_t idesc = idesc_bf16_f32(BM, (u.slots + 15) / 16 * 16);
             if (!(go = wait(acc_empty0 + 8 * acc, acc_phase ^ 1))) break;
             tc_fence_after();
-            for (int kb = 0; kb < nkb; ++kb) {
-                if (!(go = wait(full0 + 8 * st, phase))) break;
+            // Two k-steps at a time, half the warp waiting for each: between the commits of one pair and the
+            // first MMA of the next this thread spends ~450 clocks on the wait, which the pair's MMAs cover
+            for (int kb = 0; kb < nkb; kb += 2) {
+                const int two = kb + 1 < nkb, st1 = st + 1 == STAGES ? 0 : st + 1, phase1 = st1 ? phase : phase ^ 1;
+                const bool second = two && (lane & 1);
+                if (!(go = wait(full0 + 8 * (second ? st1 : st), second ? phase1 : phase))) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t a = sA + st * A_STAGE, b = sB + st * B_STAGE;
+                if (elect_one()) {
+                    // 16 k are 32 bytes of a swizzled row, 2 in the descriptor's address field
+                    uint64_t a = a_desc + (uint32_t)st * (A_STAGE >> 4), b = b_desc + (uint32_t)st * (B_STAGE >> 4);
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_f16(tmem + acc * BN, smem_desc_sw128(a + kk * 32), smem_desc_sw128(b + kk * 32), idesc,
-                                 (kb | kk) != 0);
+                        umma_f16(tmem + acc * BN, a + 2 * kk, b + 2 * kk, idesc, (kb | kk) != 0);
                     umma_commit(empty0 + 8 * st);
-                    if (kb == nkb - 1) umma_commit(acc_full0 + 8 * acc);
+                    if (two) {
+                        a = a_desc + (uint32_t)st1 * (A_STAGE >> 4), b = b_desc + (uint32_t)st1 * (B_STAGE >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            umma_f16(tmem + acc * BN, a + 2 * kk, b + 2 * kk, idesc, 1);
+                        umma_commit(empty0 + 8 * st1);
+                    }
+                    if (kb + 2 >= nkb) umma_commit(acc_full0 + 8 * acc);
                 }
                 __syncwarp();
                 advance();
+                if (two) advance();
             }
             if (++acc == 2) acc = 0, acc_phase ^= 1;
         }
@@ -218,39 +284,33 @@ __global__ void __launch_bounds__(THREADS, 1)
             umma_commit(drained);
             mbar_wait(drained, 0, status);
         }
-    } else if (warp < EPILOGUE_WARP) {
-        // ---- signs: group h takes the pairs of k-steps h, h + 2, ...
+    } else if (warp >= UNPACK_WARP && warp < (GATHER ? GATHER_WARP : EPILOGUE_WARP)) {
+        // ---- signs: of two groups, group h takes the pairs of k-steps h, h + 2, ...
         const int group = (warp - UNPACK_WARP) >> 2, row = (threadIdx.x - 32 * UNPACK_WARP) & 127;
         const uint32_t row_off = (row >> 3) * 1024 + (row & 7) * 128, sw = row & 7;
-        const bool vec = (kw & 3) == 0;  // rows of words 16-byte aligned
         const int pairs = (nkb + 1) / 2;
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
             const int r = min(u.blk * BM + row, c.out - 1);  // rows past `out` are computed but not stored
-            const long long w0 = ((long long)u.e * c.out + r) * kw, words = (long long)c.experts * c.out * kw;
+            // The words of a pair of k-steps. Past the row's end its last words are read again: u is
+            // zero there. (No branch: a load merged with another value would be waited for at once.)
+            const uint32_t* w0 = c.packed + ((long long)u.e * c.out + r) * kw;
             auto load = [&](int pair) {
                 const int x = 4 * pair;
-                uint4 v = {0, 0, 0, 0};  // u is zero past K
-                if (vec && x + 4 <= kw) {
-                    if (LQ_IN_BOUNDS(w0 + x + 3, words)) v = __ldg(reinterpret_cast<const uint4*>(c.packed + w0 + x));
-                } else if (!vec) {
-                    if (x < kw && LQ_IN_BOUNDS(w0 + x, words)) v.x = __ldg(c.packed + w0 + x);
-                    if (x + 1 < kw && LQ_IN_BOUNDS(w0 + x + 1, words)) v.y = __ldg(c.packed + w0 + x + 1);
-                    if (x + 2 < kw && LQ_IN_BOUNDS(w0 + x + 2, words)) v.z = __ldg(c.packed + w0 + x + 2);
-                    if (x + 3 < kw && LQ_IN_BOUNDS(w0 + x + 3, words)) v.w = __ldg(c.packed + w0 + x + 3);
-                }
-                return v;
+                if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(w0 + min(x, kw - 4)));
+                return make_uint4(__ldg(w0 + min(x, kw - 1)), __ldg(w0 + min(x + 1, kw - 1)), __ldg(w0 + min(x + 2, kw - 1)),
+                                  __ldg(w0 + min(x + 3, kw - 1)));
             };
             uint4 ahead[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ahead[i] = load(group + 2 * i);
+            for (int i = 0; i < 4; ++i) ahead[i] = load(group + GROUPS * i);
             const int st0 = st, phase0 = phase;  // ring position of the unit's first k-step
-            for (int p0 = group; p0 < pairs && go; p0 += 8) {
+            for (int p0 = group; p0 < pairs && go; p0 += 4 * GROUPS) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int pair = p0 + 2 * i;
+                    const int pair = p0 + GROUPS * i;
                     if (pair >= pairs || !go) break;
                     const uint32_t w[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
-                    ahead[i] = load(pair + 8);
+                    ahead[i] = load(pair + 4 * GROUPS);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int kb = 2 * pair + half;
@@ -275,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             phase = phase0 ^ ((st / STAGES) & 1);
             st %= STAGES;
         }
-    } else {
+    } else if (warp >= EPILOGUE_WARP) {
         // ---- epilogue: a warp may only reach its own quarter of the TMEM lanes (warp % 4)
         const int q = warp & 3, width = c.glu ? c.out / 2 : c.out;
         int acc = 0, acc_phase = 0;
@@ -289,16 +349,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int c0 = 0; c0 < u.slots; c0 += 32) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + acc * BN + ((uint32_t)(q * 32) << 16) + c0, v);
-                unsigned there = 0xffffffffu;
-                if (c.rows) {  // a slot whose row is outside u counts as zero
-                    const int slot = u.slot0 + c0 + lane;
-                    const int row = c0 + lane < u.slots ? __ldg(c.rows + slot) : 0;
-                    there = __ballot_sync(0xffffffffu, row >= 0 && row < c.tokens);
-                }
                 tmem_ld_wait();
                 float z[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, (there >> j) & 1u ? __uint_as_float(v[j]) : 0.f, br);
+                for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, __uint_as_float(v[j]), br);
                 store_chunk(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
             }
             tc_fence_before();
@@ -332,30 +386,50 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-}  // namespace
-
-cudaError_t launch_grouped_tc(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
-    EncodeTiledFn encode = encode_fn();
-    if (!encode) return cudaErrorNotSupported;
-    CUtensorMap map;
-    cuuint64_t gdim[2] = {(cuuint64_t)c.K, (cuuint64_t)c.tokens};
-    cuuint64_t gstride[1] = {(cuuint64_t)c.K * 2};
-    cuuint32_t box[2] = {BK, c.rows ? 1u : (cuuint32_t)kBox};
-    cuuint32_t estride[2] = {1, 1};
-    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.u), gdim, gstride, box, estride,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+template <int BN, bool VEC, bool GATHER>
+cudaError_t launch_as(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
+    CUtensorMap map, map_all;  // u in boxes of kBox, and of BN, rows; not used by gathers
+    memset(&map, 0, sizeof(map));
+    memset(&map_all, 0, sizeof(map_all));
+    if (!GATHER) {
+        EncodeTiledFn encode = encode_fn();
+        if (!encode) return cudaErrorNotSupported;
+        cuuint64_t gdim[2] = {(cuuint64_t)c.K, (cuuint64_t)c.tokens};
+        cuuint64_t gstride[1] = {(cuuint64_t)c.K * 2};
+        cuuint32_t estride[2] = {1, 1};
+        for (int i = 0; i < 2; ++i) {
+            cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)(i ? BN : kBox)};
+            if (encode(i ? &map_all : &map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.u), gdim, gstride, box,
+                       estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
+        }
+    }
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+        cudaError_t e = cudaFuncSetAttribute(tc_kernel<BN, VEC, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)Ring<BN>::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    tc_kernel<<<sms, THREADS, SMEM_BYTES, st>>>(map, c, status);
+    tc_kernel<BN, VEC, GATHER><<<sms, THREADS, Ring<BN>::SMEM_BYTES, st>>>(map, map_all, c, status);
     return cudaGetLastError();
+}
+
+template <int BN>
+cudaError_t launch_bn(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
+    if (c.rows) return c.K % 128 == 0 ? launch_as<BN, true, true>(c, status, st, sms) : launch_as<BN, false, true>(c, status, st, sms);
+    return c.K % 128 == 0 ? launch_as<BN, true, false>(c, status, st, sms) : launch_as<BN, false, false>(c, status, st, sms);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_tc(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms, int each) {
+    if (each <= 64) return launch_bn<64>(c, status, st, sms);
+    if (each <= 128) return launch_bn<128>(c, status, st, sms);
+    return launch_bn<256>(c, status, st, sms);
 }
 
 }  // namespace lq
