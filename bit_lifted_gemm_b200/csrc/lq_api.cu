@@ -497,6 +497,8 @@ size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n) {
     lq::GroupedCall c =
         layer_call(nullptr, nullptr, out, K, nullptr, true, n, nullptr, 0, 0, nullptr, nullptr, LQ_F32);
     c.experts = experts;
+    static const int some_offsets = 0;  // that there are offsets counts, not where
+    c.offsets = &some_offsets;
     return lq::grouped_workspace_size(c);
 }
 

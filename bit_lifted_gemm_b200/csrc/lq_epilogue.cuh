@@ -10,6 +10,11 @@
 
 namespace lq {
 
+// a / b to two steps of fp32 without the branches of the rounded division, which keep a
+// warp from overlapping one element's with the next one's. Denominators above 2^126 give 0, where a
+// gate of such a denominator (e^-z, z < -87) is below 10^-36.
+__device__ __forceinline__ float quotient(float a, float b) { return __fdividef(a, b); }
+
 // act(z) in fp32. The forms avoid cancellation for negative z: gelu as
 // z/2 erfc(-z/sqrt 2), gelu_tanh through 1/2 (1 + tanh y) = 1 / (1 + e^(-2y)).
 // relu keeps NaN.
@@ -19,14 +24,45 @@ __device__ __forceinline__ float activate(float z, int act) {
         case LQ_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
         case LQ_ACT_GELU_TANH: {
             const float y = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-            return z / (1.f + expf(-2.f * y));
+            return quotient(z, 1.f + expf(-2.f * y));
         }
-        case LQ_ACT_SILU: return z / (1.f + expf(-z));
+        case LQ_ACT_SILU: return quotient(z, 1.f + expf(-z));
         default: return z;
     }
 }
 
+// act on N values, the choice made once.
+template <int N>
+__device__ __forceinline__ void activate_all(float (&z)[N], int act) {
+    switch (act) {
+#define LQ_ACT_CASE(A)                                     \
+    case A:                                                \
+        _Pragma("unroll") for (int j = 0; j < N; ++j) z[j] = activate(z[j], A); \
+        break;
+        LQ_ACT_CASE(LQ_ACT_RELU)
+        LQ_ACT_CASE(LQ_ACT_GELU)
+        LQ_ACT_CASE(LQ_ACT_GELU_TANH)
+        LQ_ACT_CASE(LQ_ACT_SILU)
+#undef LQ_ACT_CASE
+        default: break;
+    }
+}
+
 __device__ __forceinline__ float bf16_to_float(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// An fp32 or bf16 element as it is stored, and its conversions.
+template <bool BF16>
+struct Elem {
+    using T = uint16_t;
+    static __device__ __forceinline__ float to_float(T v) { return bf16_to_float(v); }
+    static __device__ __forceinline__ T from_float(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+};
+template <>
+struct Elem<false> {
+    using T = float;
+    static __device__ __forceinline__ float to_float(T v) { return v; }
+    static __device__ __forceinline__ T from_float(float v) { return v; }
+};
 
 // Element i of an fp32 or bf16 array.
 __device__ __forceinline__ float load_elem(const void* p, long long i, bool bf16) {

@@ -12,19 +12,29 @@
 
 namespace lq {
 
+namespace {
+
+// Slots of an expert on average, and whether the kernel for few of them takes the call.
+int slots_each(const GroupedCall& c) {
+    const int active = c.n < c.experts ? c.n : c.experts;
+    return (int)(((long long)c.n + active - 1) / active);
+}
+bool few_rows(const GroupedCall& c) { return !c.u_bf16 || slots_each(c) <= 32; }
+
+}  // namespace
+
 size_t grouped_workspace_size(const GroupedCall& c) {
-    const size_t planes = grouped_mma_workspace_size(c.K, c.n, c.u_bf16);
-    return planes > 256 ? planes : 256;
+    const size_t need = few_rows(c) ? grouped_mma_workspace_size(c.K, c.n, c.u_bf16)
+                                    : c.offsets ? grouped_tc_workspace_size(c.K, c.n) : 0;
+    return need > 256 ? need : 256;
 }
 
 cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st) {
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int active = c.n < c.experts ? c.n : c.experts;
-    const int each = (int)(((long long)c.n + active - 1) / active);
-    if (!c.u_bf16 || each <= 32) return launch_grouped_mma(c, ws, status, st, sms);
-    return launch_grouped_tc(c, status, st, sms, each);
+    if (few_rows(c)) return launch_grouped_mma(c, ws, status, st, sms);
+    return launch_grouped_tc(c, ws, status, st, sms, slots_each(c));
 }
 
 }  // namespace lq

@@ -6,20 +6,19 @@
 // A unit is a tile of 128 weight rows by up to BN slots of one expert; persistent
 // CTAs (one per SM) take units in turn (256, 128 or 64 slots to a full tile). The MMA's width N is the tile's slots
 // rounded up to 16, so a short tail of an expert costs what it needs. K is walked in
-// steps of 64 through a ring of stages:
-//   warp 0        u rows of the slots by TMA (128-byte swizzle), without `rows`
+// steps of 64 (128 for narrow tiles) through a ring of stages. Roles:
+//   warp 0        u rows of the slots by TMA (128-byte swizzle)
 //   warp 1        issues the MMAs (M = 128, K = 16, bf16, fp32 in TMEM)
-//   warps 2..9    two groups that take pairs of k-steps in turn; a thread owns one weight
-//                 row, loads its sign words well ahead and stores them as bf16 +-1 into
-//                 the stage in the swizzled layout. With `rows`, the second group copies
-//                 the gathered rows of u instead, with 16-byte cp.async (TMA gathers of four rows took
-//                 75 clocks each, 4800 per k-step)
-//   warps 10..13  epilogue of the tile before, from the other of two accumulators:
-//                 scale, bias, activation or gate, residual, one rounding, store. A
-//                 thread owns one weight row, so a warp stores 32 neighbouring outputs.
+//   warps 2..9    two groups that take 128 k in turn; a thread owns one weight row, loads its sign
+//                 words well ahead and stores them as bf16 +-1 into the stage in the swizzled layout
+//   warps 10..13  epilogue of the tile before, from the other of two accumulators: scale, bias,
+//                 activation or gate, residual, one rounding, store. A thread owns one weight
+//                 row, so a warp stores 32 neighbouring outputs.
+// With `rows`, a kernel before it copies the slots' rows of u into the workspace: gathering
+// them in this kernel, four to a TMA instruction, took 1200 clocks per 64 k of 256 slots
+// (the MMAs take 512), and with cp.async 1900; the copy costs n K bytes written and read.
 // Products are exact; only the fp32 sums round. Every wait is bounded.
 #include <cuda.h>
-#include <string.h>
 
 #include "lq_debug.cuh"
 #include "lq_epilogue.cuh"
@@ -32,30 +31,22 @@ namespace {
 
 using namespace sm100;
 
-constexpr int BM = 128, BK = 64;
-constexpr int A_STAGE = BM * BK * 2;
+constexpr int BM = 128, BK = 64;        // BK: k of one swizzled tile
+constexpr int A_TILE = BM * BK * 2;
 constexpr int kBox = 64;  // rows of a tiled load of u of a short tile; a long one loads all BN rows at once
-constexpr int UNPACK_WARP = 2, GATHER_WARP = 6, EPILOGUE_WARP = 10;
-constexpr int THREADS = 32 * 14;
-// A stage is freed ~400 clocks after its MMAs, refilled ~1000 later: narrow tiles need more of them in flight.
+// A stage is SUB tiles of 64 k. tcgen05.commit takes its thread ~450 clocks, and four MMAs of a narrow tile
+// less: narrow tiles commit every 128 k (one thread issuing 64 k steps of N = 64: 500 clocks each).
 template <int BN>
 struct Ring {
-    static constexpr int STAGES = BN == 64 ? 8 : BN == 128 ? 6 : 4;
-    static constexpr int B_STAGE = BN * BK * 2;
+    static constexpr int SUB = BN == 256 ? 1 : 2;
+    static constexpr int STAGES = BN == 128 ? 3 : 4;
+    static constexpr int A_STAGE = SUB * A_TILE, B_TILE = BN * BK * 2, B_STAGE = SUB * B_TILE;
     static constexpr size_t SMEM_BYTES = 1024 + STAGES * (A_STAGE + B_STAGE) + 256;
 };
+constexpr int UNPACK_WARP = 2, EPILOGUE_WARP = 10, THREADS = 32 * 14;
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {  // all but the last N groups of this thread have landed
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // One lane of a converged warp, in the form that lets the compiler keep the operands of
@@ -76,52 +67,69 @@ __device__ __forceinline__ void expand16(uint32_t x, uint32_t* v) {
     }
 }
 
-// One row's outputs for 32 slots of the tile, from its accumulator columns.
-__device__ __forceinline__ void store_chunk(const GroupedCall& c, const float (&z)[32], int m, int width, int slot0,
-                                            int count, int lane) {
+// N outputs of one weight row: element at + j * width of o, for slots j below count, with the residual.
+// Every choice is made outside the loops over j: a warp works alone on its scheduler here, and
+// branches between the elements cost it 330 clocks an element (45 us for a tile of 256 slots).
+template <int N, bool BF16>
+__device__ __forceinline__ void store_row(const GroupedCall& c, float (&y)[N], long long at, int width, int count) {
+    using T = typename Elem<BF16>::T;
     const long long extent = (long long)c.n * width;
+    (void)extent;
+    T* o = static_cast<T*>(c.o) + at;
+    if (c.residual) {
+        const T* res = static_cast<const T*>(c.residual) + at;
+        T r[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) r[j] = j < count ? __ldg(res + (long long)j * width) : T(0);
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[j] += Elem<BF16>::to_float(r[j]);
+    }
+    if (count >= N) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (LQ_IN_BOUNDS(at + (long long)j * width, extent)) o[(long long)j * width] = Elem<BF16>::from_float(y[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < count && LQ_IN_BOUNDS(at + (long long)j * width, extent))
+                o[(long long)j * width] = Elem<BF16>::from_float(y[j]);
+    }
+}
+
+// One row's outputs for 32 slots of the tile, from its accumulator columns.
+template <bool BF16>
+__device__ __forceinline__ void store_chunk(const GroupedCall& c, float (&z)[32], int m, int width, int slot0, int count,
+                                            int lane) {
     if (!c.glu) {
-        if (m >= c.out) return;
-        float r[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            r[j] = c.residual && j < count ? load_elem(c.residual, (long long)(slot0 + j) * width + m, c.o_bf16) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < count && LQ_IN_BOUNDS((long long)(slot0 + j) * width + m, extent)) {
-                const float y = activate(z[j], c.act);
-                store_elem(c.o, (long long)(slot0 + j) * width + m, c.o_bf16, c.residual ? y + r[j] : y);
-            }
+        activate_all(z, c.act);
+        if (m < c.out) store_row<32, BF16>(c, z, (long long)slot0 * width + m, width, count);
         return;
     }
     // gate rows are the even lanes', the other factors the odd lanes': lane pairs swap
     // halves, the even lane finishes slots 0..15 and the odd lane slots 16..31
     const bool odd = lane & 1;
-    const int j0 = odd ? 16 : 0;
-    const bool there = m < c.out;
-    float r[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        r[j] = c.residual && there && j0 + j < count
-                   ? load_elem(c.residual, (long long)(slot0 + j0 + j) * width + m / 2, c.o_bf16)
-                   : 0.f;
+    float gate[16], up[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         const float own = odd ? z[16 + j] : z[j], other = __shfl_xor_sync(0xffffffffu, odd ? z[j] : z[16 + j], 1);
-        if (!there || j0 + j >= count || !LQ_IN_BOUNDS((long long)(slot0 + j0 + j) * width + m / 2, extent)) continue;
-        const float y = activate(odd ? other : own, c.act) * (odd ? own : other);
-        store_elem(c.o, (long long)(slot0 + j0 + j) * width + m / 2, c.o_bf16, c.residual ? y + r[j] : y);
+        gate[j] = odd ? other : own;
+        up[j] = odd ? own : other;
     }
+    activate_all(gate, c.act);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) gate[j] *= up[j];
+    const int j0 = odd ? 16 : 0;
+    if (m < c.out) store_row<16, BF16>(c, gate, (long long)(slot0 + j0) * width + m / 2, width, count - j0);
 }
 
 // BN: slots of a full tile. VEC: K a multiple of 128, so that rows of sign words are
 // 16-byte aligned. GATHER: rows are given.
-template <int BN, bool VEC, bool GATHER>
+template <int BN, bool VEC>
 __global__ void __launch_bounds__(THREADS, 1)
     tc_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_all,
               const __grid_constant__ GroupedCall c, unsigned* status) {
-    constexpr int STAGES = Ring<BN>::STAGES, B_STAGE = Ring<BN>::B_STAGE;
-    constexpr int GROUPS = GATHER ? 1 : 2;  // of unpack warps
+    constexpr int STAGES = Ring<BN>::STAGES, SUB = Ring<BN>::SUB, A_STAGE = Ring<BN>::A_STAGE;
+    constexpr int B_STAGE = Ring<BN>::B_STAGE, B_TILE = Ring<BN>::B_TILE, STEP = SUB * BK;
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned for the 128-byte swizzle
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -133,11 +141,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t acc_full0 = empty0 + 8 * STAGES, acc_empty0 = acc_full0 + 16, drained = acc_empty0 + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kw = c.K >> 5, nkb = (c.K + BK - 1) / BK, nblk = (c.out + BM - 1) / BM;
+    const int kw = c.K >> 5, nkb = (c.K + STEP - 1) / STEP, nblk = (c.out + BM - 1) / BM;
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < STAGES; ++st) {
-            mbar_init(full0 + 8 * st, GATHER ? 256 : 1 + 128);
+            mbar_init(full0 + 8 * st, 1 + 128);
             mbar_init(empty0 + 8 * st, 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -175,22 +183,42 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++st == STAGES) st = 0, phase ^= 1;
     };
     bool go = true;
-    if (!GATHER && warp == 0) {
+    // The same for a role's next stage, with the poll before the work on the current one: after a commit
+    // a poll takes hundreds of clocks, which would come between the MMAs of two stages. poll() looks at the
+    // stage after this one, ready() waits for the current stage unless the last poll saw it complete.
+    bool seen = false;
+    auto poll = [&](uint32_t bar0, uint32_t flip) {
+        const int st1 = st + 1 == STAGES ? 0 : st + 1;
+        seen = mbar_try_wait(bar0 + 8 * st1, (st1 ? phase : phase ^ 1) ^ flip);
+    };
+    auto ready = [&](uint32_t bar0, uint32_t flip) {
+        const bool known = __all_sync(0xffffffffu, seen);
+        seen = false;
+        return known || wait(bar0 + 8 * st, phase ^ flip);
+    };
+    if (warp == 0) {
         // ---- u tiles
         int issued = 0;
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
             const bool all = u.slots > BN - kBox;
             const int boxes = all ? BN / kBox : (u.slots + kBox - 1) / kBox;
             for (int kb = 0; kb < nkb; ++kb) {
-                if (!(go = wait(empty0 + 8 * st, phase ^ 1))) break;
-                const uint32_t dst = sB + st * B_STAGE, bar = full0 + 8 * st;
-                if (lane == 0) mbar_arrive_expect_tx(bar, boxes * kBox * 128);
-                __syncwarp();
-                if (all) {
-                    if (lane == 0) tma_load_2d(dst, &tmap_all, kb * BK, u.slot0, bar);
-                } else if (lane < boxes) {
-                    tma_load_2d(dst + lane * kBox * 128, &tmap_u, kb * BK, u.slot0 + lane * kBox, bar);
+                if (!(go = ready(empty0, 1))) break;
+                poll(empty0, 1);
+                if (elect_one()) {
+                    const uint32_t dst = sB + st * B_STAGE, bar = full0 + 8 * st;
+                    mbar_arrive_expect_tx(bar, SUB * boxes * kBox * 128);
+#pragma unroll
+                    for (int x = 0; x < SUB; ++x) {
+                        const uint32_t to = dst + x * B_TILE;
+                        if (all)
+                            tma_load_2d(to, &tmap_all, kb * STEP + x * BK, u.slot0, bar);
+                        else
+                            for (int i = 0; i < boxes; ++i)
+                                tma_load_2d(to + i * kBox * 128, &tmap_u, kb * STEP + x * BK, u.slot0 + i * kBox, bar);
+                    }
                 }
+                __syncwarp();
                 ++issued;
                 advance();
             }
@@ -200,49 +228,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int at = issued - back;
             mbar_wait(full0 + 8 * (at % STAGES), (at / STAGES) & 1, status);
         }
-    } else if (GATHER && warp >= GATHER_WARP && warp < EPILOGUE_WARP) {
-        // ---- gathered rows of u: a thread copies one 16-byte chunk of every 16th row, in the
-        // layout that a 128-byte swizzled tile has; stages are handed over LAG steps later, when they have landed
-        constexpr int LAG = STAGES - 2, ROWS = BN / 16;
-        const int tid = threadIdx.x - 32 * GATHER_WARP, chunk = tid & 7, first = tid >> 3;
-        const uint32_t off = first * 128 + ((chunk ^ (first & 7)) << 4);
-        const uint16_t* ub = static_cast<const uint16_t*>(c.u);
-        int given = 0, issued = 0;  // k-steps handed over, and begun
-        auto hand_over = [&] {
-            fence_proxy_async_smem();
-            mbar_arrive(full0 + 8 * (given % STAGES));
-            ++given;
-        };
-        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
-            const int pad = (u.slots + 15) / 16;
-            int rows[ROWS];  // -1: a zero row
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const int j = first + 16 * i;
-                const int row = j < u.slots ? __ldg(c.rows + u.slot0 + j) : -1;
-                rows[i] = row >= 0 && row < c.tokens ? row : -1;
-            }
-            for (int kb = 0; kb < nkb; ++kb) {
-                if (!(go = wait(empty0 + 8 * st, phase ^ 1))) break;
-                const uint32_t dst = sB + st * B_STAGE + off;
-                const int k = kb * BK + chunk * 8;
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i)
-                    if (i < pad) {
-                        const bool there = rows[i] >= 0 && k < c.K &&
-                                           LQ_IN_BOUNDS((long long)rows[i] * c.K + k + 7, (long long)c.tokens * c.K);
-                        cp_async16(dst + i * 2048, there ? ub + (long long)rows[i] * c.K + k : ub, there);
-                    }
-                cp_async_commit();
-                advance();
-                if (++issued > LAG) {
-                    cp_async_wait<LAG>();
-                    hand_over();
-                }
-            }
-        }
-        cp_async_wait<0>();
-        while (given < issued) hand_over();
     } else if (warp == 1) {
         // ---- MMAs
         int acc = 0, acc_phase = 0;
@@ -251,32 +236,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t idesc = idesc_bf16_f32(BM, (u.slots + 15) / 16 * 16);
             if (!(go = wait(acc_empty0 + 8 * acc, acc_phase ^ 1))) break;
             tc_fence_after();
-            // Two k-steps at a time, half the warp waiting for each: between the commits of one pair and the
-            // first MMA of the next this thread spends ~450 clocks on the wait, which the pair's MMAs cover
-            for (int kb = 0; kb < nkb; kb += 2) {
-                const int two = kb + 1 < nkb, st1 = st + 1 == STAGES ? 0 : st + 1, phase1 = st1 ? phase : phase ^ 1;
-                const bool second = two && (lane & 1);
-                if (!(go = wait(full0 + 8 * (second ? st1 : st), second ? phase1 : phase))) break;
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!(go = ready(full0, 0))) break;
+                poll(full0, 0);
                 tc_fence_after();
                 if (elect_one()) {
                     // 16 k are 32 bytes of a swizzled row, 2 in the descriptor's address field
-                    uint64_t a = a_desc + (uint32_t)st * (A_STAGE >> 4), b = b_desc + (uint32_t)st * (B_STAGE >> 4);
+                    const uint64_t a = a_desc + (uint32_t)st * (A_STAGE >> 4), b = b_desc + (uint32_t)st * (B_STAGE >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_f16(tmem + acc * BN, a + 2 * kk, b + 2 * kk, idesc, (kb | kk) != 0);
-                    umma_commit(empty0 + 8 * st);
-                    if (two) {
-                        a = a_desc + (uint32_t)st1 * (A_STAGE >> 4), b = b_desc + (uint32_t)st1 * (B_STAGE >> 4);
+                    for (int x = 0; x < SUB; ++x)
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-                            umma_f16(tmem + acc * BN, a + 2 * kk, b + 2 * kk, idesc, 1);
-                        umma_commit(empty0 + 8 * st1);
-                    }
-                    if (kb + 2 >= nkb) umma_commit(acc_full0 + 8 * acc);
+                            umma_f16(tmem + acc * BN, a + x * (A_TILE >> 4) + 2 * kk, b + x * (B_TILE >> 4) + 2 * kk, idesc,
+                                     (kb | x | kk) != 0);
+                    umma_commit(empty0 + 8 * st);
+                    if (kb == nkb - 1) umma_commit(acc_full0 + 8 * acc);
                 }
                 __syncwarp();
                 advance();
-                if (two) advance();
             }
             if (++acc == 2) acc = 0, acc_phase ^= 1;
         }
@@ -284,14 +261,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             umma_commit(drained);
             mbar_wait(drained, 0, status);
         }
-    } else if (warp >= UNPACK_WARP && warp < (GATHER ? GATHER_WARP : EPILOGUE_WARP)) {
-        // ---- signs: of two groups, group h takes the pairs of k-steps h, h + 2, ...
+    } else if (warp < EPILOGUE_WARP) {
+        // ---- signs, 128 k at a time (one 16-byte load); of two groups, each takes every other one
+        constexpr int GROUPS = 2;
         const int group = (warp - UNPACK_WARP) >> 2, row = (threadIdx.x - 32 * UNPACK_WARP) & 127;
         const uint32_t row_off = (row >> 3) * 1024 + (row & 7) * 128, sw = row & 7;
-        const int pairs = (nkb + 1) / 2;
+        const int pairs = (c.K + 127) / 128;
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
             const int r = min(u.blk * BM + row, c.out - 1);  // rows past `out` are computed but not stored
-            // The words of a pair of k-steps. Past the row's end its last words are read again: u is
+            // The words of 128 k. Past the row's end its last words are read again: u is
             // zero there. (No branch: a load merged with another value would be waited for at once.)
             const uint32_t* w0 = c.packed + ((long long)u.e * c.out + r) * kw;
             auto load = [&](int pair) {
@@ -313,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ahead[i] = load(pair + 4 * GROUPS);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const int kb = 2 * pair + half;
+                        const int kb = SUB == 2 ? pair : 2 * pair + half;
                         if (kb >= nkb || !go) break;
                         const int at = st0 + kb, s = at % STAGES, ph = phase0 ^ ((at / STAGES) & 1);
                         uint32_t v[32];
@@ -321,13 +299,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                         expand16(w[2 * half] >> 16, v + 8);
                         expand16(w[2 * half + 1], v + 16);
                         expand16(w[2 * half + 1] >> 16, v + 24);
-                        if (!(go = wait(empty0 + 8 * s, ph ^ 1))) break;
-                        const uint32_t dst = sA + s * A_STAGE + row_off;
+                        if (SUB == 1 || half == 0)
+                            if (!(go = wait(empty0 + 8 * s, ph ^ 1))) break;
+                        const uint32_t dst = sA + s * A_STAGE + (SUB == 2 ? half * A_TILE : 0) + row_off;
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             st_shared_v4(dst + ((q ^ sw) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                        fence_proxy_async_smem();
-                        mbar_arrive(full0 + 8 * s);
+                        if (SUB == 1 || half == 1) {
+                            fence_proxy_async_smem();
+                            mbar_arrive(full0 + 8 * s);
+                        }
                     }
                 }
             }
@@ -335,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             phase = phase0 ^ ((st / STAGES) & 1);
             st %= STAGES;
         }
-    } else if (warp >= EPILOGUE_WARP) {
+    } else {
         // ---- epilogue: a warp may only reach its own quarter of the TMEM lanes (warp % 4)
         const int q = warp & 3, width = c.glu ? c.out / 2 : c.out;
         int acc = 0, acc_phase = 0;
@@ -353,7 +334,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float z[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, __uint_as_float(v[j]), br);
-                store_chunk(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
+                if (c.o_bf16)
+                    store_chunk<true>(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
+                else
+                    store_chunk<false>(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
             }
             tc_fence_before();
             mbar_arrive(acc_empty0 + 8 * acc);
@@ -386,47 +370,69 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-template <int BN, bool VEC, bool GATHER>
-cudaError_t launch_as(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
-    CUtensorMap map, map_all;  // u in boxes of kBox, and of BN, rows; not used by gathers
-    memset(&map, 0, sizeof(map));
-    memset(&map_all, 0, sizeof(map_all));
-    if (!GATHER) {
-        EncodeTiledFn encode = encode_fn();
-        if (!encode) return cudaErrorNotSupported;
-        cuuint64_t gdim[2] = {(cuuint64_t)c.K, (cuuint64_t)c.tokens};
-        cuuint64_t gstride[1] = {(cuuint64_t)c.K * 2};
-        cuuint32_t estride[2] = {1, 1};
-        for (int i = 0; i < 2; ++i) {
-            cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)(i ? BN : kBox)};
-            if (encode(i ? &map_all : &map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.u), gdim, gstride, box,
-                       estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-                return cudaErrorInvalidValue;
+// Slot i's row of u, zeros for a row outside it; slots of no expert are left as they are.
+__global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ GroupedCall c, uint4* __restrict__ dst) {
+    const int chunks = c.K / 8;
+    const int end = min(max(__ldg(c.offsets + c.experts), 0), c.n);
+    for (int i = blockIdx.x; i < end; i += gridDim.x) {
+        const int row = __ldg(c.rows + i);
+        const bool there = row >= 0 && row < c.tokens;
+        const uint4* src = reinterpret_cast<const uint4*>(c.u) + (there ? (long long)row * chunks : 0);
+        for (int x = threadIdx.x; x < chunks; x += 256) {
+            uint4 v = {0, 0, 0, 0};
+            if (there && LQ_IN_BOUNDS((long long)row * chunks + x, (long long)c.tokens * chunks)) v = __ldg(src + x);
+            if (LQ_IN_BOUNDS((long long)i * chunks + x, (long long)c.n * chunks)) dst[(long long)i * chunks + x] = v;
         }
+    }
+}
+
+template <int BN, bool VEC>
+cudaError_t launch_as(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
+    EncodeTiledFn encode = encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    CUtensorMap map, map_all;  // u in boxes of kBox and of BN rows
+    cuuint64_t gdim[2] = {(cuuint64_t)c.K, (cuuint64_t)c.tokens};
+    cuuint64_t gstride[1] = {(cuuint64_t)c.K * 2};
+    cuuint32_t estride[2] = {1, 1};
+    for (int i = 0; i < 2; ++i) {
+        cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)(i ? BN : kBox)};
+        if (encode(i ? &map_all : &map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.u), gdim, gstride, box,
+                   estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
     }
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(tc_kernel<BN, VEC, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(tc_kernel<BN, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)Ring<BN>::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    tc_kernel<BN, VEC, GATHER><<<sms, THREADS, Ring<BN>::SMEM_BYTES, st>>>(map, map_all, c, status);
+    tc_kernel<BN, VEC><<<sms, THREADS, Ring<BN>::SMEM_BYTES, st>>>(map, map_all, c, status);
     return cudaGetLastError();
 }
 
 template <int BN>
 cudaError_t launch_bn(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
-    if (c.rows) return c.K % 128 == 0 ? launch_as<BN, true, true>(c, status, st, sms) : launch_as<BN, false, true>(c, status, st, sms);
-    return c.K % 128 == 0 ? launch_as<BN, true, false>(c, status, st, sms) : launch_as<BN, false, false>(c, status, st, sms);
+    return c.K % 128 == 0 ? launch_as<BN, true>(c, status, st, sms) : launch_as<BN, false>(c, status, st, sms);
 }
 
 }  // namespace
 
-cudaError_t launch_grouped_tc(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms, int each) {
+size_t grouped_tc_workspace_size(int K, int n) { return (size_t)n * K * 2; }
+
+cudaError_t launch_grouped_tc(const GroupedCall& call, void* ws, unsigned* status, cudaStream_t st, int sms, int each) {
+    GroupedCall c = call;
+    if (c.rows) {
+        gather_kernel<<<c.n < 8 * sms ? c.n : 8 * sms, 256, 0, st>>>(c, static_cast<uint4*>(ws));
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        c.u = ws;
+        c.tokens = c.n;
+        c.rows = nullptr;
+    }
     if (each <= 64) return launch_bn<64>(c, status, st, sms);
     if (each <= 128) return launch_bn<128>(c, status, st, sms);
     return launch_bn<256>(c, status, st, sms);

@@ -130,7 +130,8 @@ cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cud
 size_t grouped_mma_workspace_size(int K, int n, bool u_bf16);
 cudaError_t launch_grouped_mma(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st, int sms);
 // Its kernel for many rows per expert (lq_grouped_tc.cu): bf16 u, about `each` slots to an expert.
-cudaError_t launch_grouped_tc(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms, int each);
+size_t grouped_tc_workspace_size(int K, int n);  // used when rows are given
+cudaError_t launch_grouped_tc(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st, int sms, int each);
 
 // Rows grouped by expert id, and the experts' rows joined per token (lq_rows.cu).
 cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts, int* offsets, int* rows, int* slots,
