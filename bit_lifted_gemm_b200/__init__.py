@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -304,6 +305,9 @@ def encode(w, M, K, err=False, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ fused epilogues and grouped products
+#
+# At decode sizes the kernels take a few microseconds, so these calls keep their own work on
+# the host small: plain comparisons, one allocation per output, addresses passed as integers.
 
 def _on(t, stream):
     """Context in which `t`'s device is current, with `stream` (if given) as the
@@ -318,22 +322,36 @@ def _on(t, stream):
     return contextlib.nullcontext()
 
 
-def _operand(t, name, dtype, shape, device):
-    """Checks one operand of the calls below (None passes): contiguous, on `device`, of this type and shape."""
-    if t is None:
-        return
-    if not t.is_cuda or not t.is_contiguous():
+def _elsewhere(t, stream, name):
+    """Whether a call on `t` has to enter another device or stream first (see _on)."""
+    import torch
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.device != device or t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, "
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
+def _raw_stream(device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _operand(t, name, dtype, shape, device):
+    """Address of one operand: a contiguous tensor on CUDA device `device`, of this type and shape; None for None."""
+    if t is None:
+        return None
+    if t.get_device() != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _float_type(o_dtype, name="o_dtype"):
     import torch
-    if o_dtype in ("f32", torch.float32):
+    if o_dtype == "f32" or o_dtype == torch.float32:
         return torch.float32, LQ_F32
-    if o_dtype in ("bf16", torch.bfloat16):
+    if o_dtype == "bf16" or o_dtype == torch.bfloat16:
         return torch.bfloat16, LQ_BF16
     raise ValueError(f"{name} must be 'f32' or 'bf16'")
 
@@ -344,50 +362,57 @@ def _activation(act):
     return ACTIVATIONS[act]
 
 
+@functools.lru_cache(maxsize=1024)
 def gemm_epilogue_workspace_size(out_rows: int, K: int, tokens: int) -> int:
     """Bytes of workspace gemm_epilogue needs (0: refused sizes)."""
     return int(lib.lq_gemm_epilogue_workspace_size(out_rows, K, tokens))
 
 
+@functools.lru_cache(maxsize=1024)
 def gemv_epilogue_workspace_size(out_rows: int, K: int, batch: int) -> int:
     """Bytes of workspace gemv_epilogue needs (0: refused sizes)."""
     return int(lib.lq_gemv_epilogue_workspace_size(out_rows, K, batch))
 
 
+@functools.lru_cache(maxsize=1024)
 def gemm_grouped_workspace_size(experts: int, out_rows: int, K: int, n: int) -> int:
     """Bytes of workspace gemm_grouped needs (0: refused sizes)."""
     return int(lib.lq_gemm_grouped_workspace_size(experts, out_rows, K, n))
 
 
-def _scratch(ws, need, device):
+def _scratch(ws, need, like):
+    """The workspace given, or a new one beside `like` (the caching allocator aligns to 512 bytes)."""
     import torch
     if ws is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)  # 512-byte aligned
+        return like.new_empty(need or 1, dtype=torch.uint8)
     _dev_tensor(ws, "workspace")
-    if ws.device != device:
-        raise ValueError(f"workspace must be on {device}")
+    if ws.device != like.device:
+        raise ValueError(f"workspace must be on {like.device}")
     return ws
 
 
 def _layer_epilogue(fn, size_fn, u_type, packed, s, u, bias, act, glu, residual, o_dtype, out, workspace, stream):
     import torch
+    if _elsewhere(u, stream, "u"):
+        with _on(u, stream):
+            return _layer_epilogue(fn, size_fn, u_type, packed, s, u, bias, act, glu, residual, o_dtype, out, workspace,
+                                   None)
     if u.dim() != 2 or packed.dim() != 2:
         raise ValueError("packed must be [out][K/32] and u [tokens][K]")
     tokens, K = u.shape
-    rows, dev = packed.shape[0], u.device
+    rows, dev = packed.shape[0], u.get_device()
     ot, o_t = _float_type(o_dtype if out is None else out.dtype)
     width = rows // 2 if glu else rows
-    with _on(u, stream):
-        if out is None:
-            out = torch.empty((tokens, width), dtype=ot, device=dev)
-        for t, name, dtype, shape in ((u, "u", u_type, (tokens, K)), (packed, "packed", torch.int32, (rows, K // 32)),
-                                      (s, "s", torch.float32, (rows,)), (bias, "bias", torch.float32, (rows,)),
-                                      (residual, "residual", ot, (tokens, width)), (out, "out", ot, (tokens, width))):
-            _operand(t, name, dtype, shape, dev)
-        ws = _scratch(workspace, size_fn(rows, K, tokens), dev)
-        _check(getattr(lib, fn)(_ptr(packed), _ptr(s), rows, K, _ptr(u), tokens, _ptr(bias), _activation(act),
-                                int(bool(glu)), _ptr(residual), _ptr(out), o_t, _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(stream)), fn)
+    if out is None:
+        out = u.new_empty((tokens, width), dtype=ot)
+    ws = _scratch(workspace, size_fn(rows, K, tokens), u)
+    f32 = torch.float32
+    _check(getattr(lib, fn)(_operand(packed, "packed", torch.int32, (rows, K // 32), dev), _operand(s, "s", f32, (rows,), dev),
+                            rows, K, _operand(u, "u", u_type, (tokens, K), dev), tokens,
+                            _operand(bias, "bias", f32, (rows,), dev), _activation(act), 1 if glu else 0,
+                            _operand(residual, "residual", ot, (tokens, width), dev),
+                            _operand(out, "out", ot, (tokens, width), dev), o_t, ws.data_ptr(),
+                            ws.numel() * ws.element_size(), _raw_stream(dev)), fn)
     return out
 
 
@@ -423,28 +448,27 @@ def gemm_grouped(packed, s, u, offsets, n, rows=None, bias=None, act=None, glu=F
     [experts][out]). offsets and rows, as group_rows gives them, stay on the device.
     Slots of no expert are not written: uninitialized when `out` is allocated here."""
     import torch
+    if _elsewhere(u, stream, "u"):
+        with _on(u, stream):
+            return gemm_grouped(packed, s, u, offsets, n, rows, bias, act, glu, o_dtype, out, workspace)
     if u.dim() != 2 or packed.dim() != 3:
         raise ValueError("packed must be [experts][out][K/32] and u [tokens][K]")
     tokens, K = u.shape
     experts, out_rows = packed.shape[:2]
-    n, dev = int(n), u.device
+    n, dev = int(n), u.get_device()
     ot, o_t = _float_type(o_dtype if out is None else out.dtype)
     width = out_rows // 2 if glu else out_rows
-    with _on(u, stream):
-        if out is None:
-            out = torch.empty((n, width), dtype=ot, device=dev)
-        for t, name, dtype, shape in ((u, "u", torch.bfloat16, (tokens, K)),
-                                      (packed, "packed", torch.int32, (experts, out_rows, K // 32)),
-                                      (s, "s", torch.float32, (experts, out_rows)),
-                                      (offsets, "offsets", torch.int32, (experts + 1,)),
-                                      (rows, "rows", torch.int32, (n,)),
-                                      (bias, "bias", torch.float32, (experts, out_rows)),
-                                      (out, "out", ot, (n, width))):
-            _operand(t, name, dtype, shape, dev)
-        ws = _scratch(workspace, gemm_grouped_workspace_size(experts, out_rows, K, n), dev)
-        _check(lib.lq_gemm_grouped(_ptr(packed), _ptr(s), experts, out_rows, K, _ptr(u), tokens, _ptr(rows),
-                                   _ptr(offsets), n, _ptr(bias), _activation(act), int(bool(glu)), _ptr(out), o_t,
-                                   _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "lq_gemm_grouped")
+    if out is None:
+        out = u.new_empty((n, width), dtype=ot)
+    ws = _scratch(workspace, gemm_grouped_workspace_size(experts, out_rows, K, n), u)
+    f32, i32 = torch.float32, torch.int32
+    _check(lib.lq_gemm_grouped(_operand(packed, "packed", i32, (experts, out_rows, K // 32), dev),
+                               _operand(s, "s", f32, (experts, out_rows), dev), experts, out_rows, K,
+                               _operand(u, "u", torch.bfloat16, (tokens, K), dev), tokens,
+                               _operand(rows, "rows", i32, (n,), dev), _operand(offsets, "offsets", i32, (experts + 1,), dev),
+                               n, _operand(bias, "bias", f32, (experts, out_rows), dev), _activation(act), 1 if glu else 0,
+                               _operand(out, "out", ot, (n, width), dev), o_t, ws.data_ptr(),
+                               ws.numel() * ws.element_size(), _raw_stream(dev)), "lq_gemm_grouped")
     return out
 
 
@@ -454,18 +478,23 @@ def group_rows(expert_ids, experts, offsets=None, rows=None, slots=None, stream=
     order, rows the token of each slot (-1 past the last), slots the slot of each choice (-1 for
     ids outside 0..experts-1)."""
     import torch
+    if _elsewhere(expert_ids, stream, "expert_ids"):
+        with _on(expert_ids, stream):
+            return group_rows(expert_ids, experts, offsets, rows, slots)
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be [tokens][topk]")
     tokens, topk = expert_ids.shape
-    dev = expert_ids.device
-    with _on(expert_ids, stream):
-        new = lambda t, shape: torch.empty(shape, dtype=torch.int32, device=dev) if t is None else t  # noqa: E731
-        offsets, rows, slots = new(offsets, (experts + 1,)), new(rows, (tokens * topk,)), new(slots, (tokens, topk))
-        for t, name, shape in ((expert_ids, "expert_ids", (tokens, topk)), (offsets, "offsets", (experts + 1,)),
-                               (rows, "rows", (tokens * topk,)), (slots, "slots", (tokens, topk))):
-            _operand(t, name, torch.int32, shape, dev)
-        _check(lib.lq_group_rows(_ptr(expert_ids), tokens, topk, experts, _ptr(offsets), _ptr(rows), _ptr(slots),
-                                 _stream(stream)), "lq_group_rows")
+    dev, i32 = expert_ids.get_device(), torch.int32
+    if offsets is None:
+        offsets = expert_ids.new_empty((experts + 1,))
+    if rows is None:
+        rows = expert_ids.new_empty((tokens * topk,))
+    if slots is None:
+        slots = expert_ids.new_empty((tokens, topk))
+    _check(lib.lq_group_rows(_operand(expert_ids, "expert_ids", i32, (tokens, topk), dev), tokens, topk, experts,
+                             _operand(offsets, "offsets", i32, (experts + 1,), dev),
+                             _operand(rows, "rows", i32, (tokens * topk,), dev),
+                             _operand(slots, "slots", i32, (tokens, topk), dev), _raw_stream(dev)), "lq_group_rows")
     return offsets, rows, slots
 
 
@@ -474,21 +503,22 @@ def combine_rows(y, slots, weights, residual=None, out=None, stream=None):
     int32 [tokens][topk] (values outside 0..n-1 add nothing), weights fp32 [tokens][topk], residual and o
     [tokens][width] in y's type."""
     import torch
+    if _elsewhere(y, stream, "y"):
+        with _on(y, stream):
+            return combine_rows(y, slots, weights, residual, out)
     if y.dim() != 2 or slots.dim() != 2:
         raise ValueError("y must be [n][width] and slots [tokens][topk]")
     n, width = y.shape
     tokens, topk = slots.shape
-    dev = y.device
+    dev = y.get_device()
     yt, y_t = _float_type(y.dtype, "y's type")
-    with _on(y, stream):
-        if out is None:
-            out = torch.empty((tokens, width), dtype=yt, device=dev)
-        for t, name, dtype, shape in ((y, "y", yt, (n, width)), (slots, "slots", torch.int32, (tokens, topk)),
-                                      (weights, "weights", torch.float32, (tokens, topk)),
-                                      (residual, "residual", yt, (tokens, width)), (out, "out", yt, (tokens, width))):
-            _operand(t, name, dtype, shape, dev)
-        _check(lib.lq_combine_rows(_ptr(y), y_t, n, width, _ptr(slots), _ptr(weights), tokens, topk, _ptr(residual),
-                                   _ptr(out), _stream(stream)), "lq_combine_rows")
+    if out is None:
+        out = y.new_empty((tokens, width))
+    _check(lib.lq_combine_rows(_operand(y, "y", yt, (n, width), dev), y_t, n, width,
+                               _operand(slots, "slots", torch.int32, (tokens, topk), dev),
+                               _operand(weights, "weights", torch.float32, (tokens, topk), dev), tokens, topk,
+                               _operand(residual, "residual", yt, (tokens, width), dev),
+                               _operand(out, "out", yt, (tokens, width), dev), _raw_stream(dev)), "lq_combine_rows")
     return out
 
 
