@@ -24,8 +24,7 @@ bool few_rows(const GroupedCall& c) { return !c.u_bf16 || slots_each(c) <= 32; }
 }  // namespace
 
 size_t grouped_workspace_size(const GroupedCall& c) {
-    const size_t need = few_rows(c) ? grouped_mma_workspace_size(c.K, c.n, c.u_bf16)
-                                    : c.offsets ? grouped_tc_workspace_size(c.K, c.n) : 0;
+    const size_t need = !few_rows(c) && c.offsets ? grouped_tc_workspace_size(c.K, c.n) : 0;
     return need > 256 ? need : 256;
 }
 
@@ -33,7 +32,7 @@ cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cud
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (few_rows(c)) return launch_grouped_mma(c, ws, status, st, sms);
+    if (few_rows(c)) return launch_grouped_mma(c, status, st, sms);
     return launch_grouped_tc(c, ws, status, st, sms, slots_each(c));
 }
 

@@ -5,21 +5,21 @@
 //
 // The weights are read once per pass of at most 8 NT columns and bound the kernel,
 // so the contraction is arranged around them: signs become the A operand of
-// mma.sync m16n8k16 (bf16, fp32 accumulate), 16 weight rows by 16 k, and up to 8
-// rows of u are its 8 columns. +-1 and u are exact in bf16, so only the fp32 sums
-// round; NaN and Inf propagate as IEEE sums do.
+// mma.sync m16n8k16 (bf16, fp32 accumulate), 16 weight rows by 16 k, and rows of u
+// are its columns. +-1 and u are exact in bf16, so only the fp32 sums round; NaN and Inf
+// propagate as IEEE sums do. An fp32 u takes three columns, bf16 parts that add up to it.
 //
-// A block is 16 H weight rows by one pass of one expert; blocks go round the
-// CTAs (one per SM). K is walked in runs of 1024 (32 sign words). Four producer
-// warps copy a run's words [16 H][32] and its slice of u's rows [cols][1024] into
-// a ring of shared-memory stages with cp.async (16-byte pieces; 8 or 4 bytes where
-// a row of words is not 16-byte aligned), zeros past K and past the last row. Eight
-// consumer warps are two groups of four that take alternate runs; the four warps of a
-// group take a quarter of the run each (8 words, 256 k) of all 16 H rows. A warp
-// keeps its u fragments of the run in registers while it walks the rows, so each
-// sign word is expanded once and each u fragment loaded once per 16 H rows.
-// At the end of a block the eight warps' sums are added in warp order through
-// shared memory (the result does not depend on timing), and the epilogue runs.
+// A block is up to H tiles of 16 weight rows by one pass of one expert; blocks go round the
+// CTAs (one per SM). K is walked in runs of 1024 (32 sign words) through a ring of
+// shared-memory stages. Four producer warps fill them: one thread loads the block's
+// words of the run [16 h][32] by TMA (128-byte swizzle; 4-byte cp.async in the same layout
+// where rows of words are not 16-byte aligned), all of them copy the run's slice of u's
+// rows [cols][1024] with cp.async, zeros past K, or split fp32 rows on the way. The consumer
+// warps form groups of four that take the runs in turn; the four warps of a group take a
+// quarter of the run each (8 words, 256 k) of all rows. A warp keeps its u fragments of the run in
+// registers while it walks the rows, so each sign word is expanded once and each u fragment
+// loaded once per 16 h rows. At the end of a block the warps' sums are added in warp
+// order through shared memory (the result does not depend on timing), and the epilogue runs.
 //
 // Order of k. Thread (g, t) = (lane / 4, lane % 4) owns words t and 4 + t of the
 // warp's eight. Register j of a word holds bits j and j + 16 at the sign positions
@@ -28,6 +28,8 @@
 // picked from two 16-byte loads. Threads with t >= 2 load the upper half of a word's u
 // first, which keeps the eight lanes of a load phase on different banks; their
 // words are rotated by 16 to match.
+#include <cuda.h>
+
 #include "lq_debug.cuh"
 #include "lq_epilogue.cuh"
 #include "lq_grouped.cuh"
@@ -40,19 +42,25 @@ namespace {
 using namespace sm100;
 
 constexpr int kRunWords = 32, kRunK = 1024;  // one stage of K
-constexpr int kConsumers = 8, kProducers = 4;
-constexpr int kThreads = 32 * (kConsumers + kProducers);
-constexpr int kUPitch = kRunK * 2 + 16;  // bytes of one u row of a stage: 16 off a multiple of 32
+constexpr int kProducers = 4;                // warps
+constexpr int kUPitch = kRunK * 2 + 16;      // bytes of one u row of a stage: 16 off a multiple of 32
 constexpr int kMaxStages = 16;
-constexpr size_t kSmemMax = 227 * 1024 - 1024;
+constexpr size_t kSmemMax = 227 * 1024 - 2048;
+constexpr size_t kHead = 512;  // barriers
+
+// H: tiles of 16 rows that a block may have. One n8 tile of columns leaves registers for three
+// groups of consumers (128 a thread), two n8 tiles for two groups (168).
+template <int NT>
+struct Shape {
+    static constexpr int COLS = 8 * NT, H = NT == 1 ? 8 : 6, GROUPS = NT == 1 ? 3 : 2;
+    static constexpr int CONSUMERS = 4 * GROUPS, THREADS = 32 * (CONSUMERS + kProducers);
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-template <int B>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(there ? B : 0)
-                 : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 // Arrives on the barrier once every earlier cp.async of this thread has landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
@@ -62,8 +70,7 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -79,11 +86,15 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 
 struct Plan {
     uint32_t shift[16];  // 2^(15 - j): kept from the compiler, so that it multiplies (see sign_pair)
-    int stages, stage_bytes, cols_cap, cols_pass, nblk;
-    int planes;  // columns per slot: 1, or 3 bf16 parts of an fp32 u
+    int stages, stage_bytes, rp;    // rp: pitch of a column of the warps' sums, in floats
+    int per, planes;                // slots of a pass, columns of a slot
+    int nblk, tiles, hmax;          // blocks and tiles of an expert's rows; a block has hmax tiles or one less
     size_t smem;
 };
 
@@ -98,101 +109,189 @@ __device__ __forceinline__ uint32_t sign_pair(uint32_t w, const Plan& p, int j) 
     return r;
 }
 
-template <int H, int NT, int VEC>
-__global__ void __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant__ GroupedCall c, const __grid_constant__ Plan p, unsigned* status) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int R = 16 * H, RP = R + 4, COLS = 8 * NT;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 16 * kMaxStages);
-    float* red = reinterpret_cast<float*>(smem + 512);  // [8 warps][COLS][RP]
-    const uint32_t ring = smem_addr(smem) + 512 + kConsumers * COLS * RP * 4;
-    const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kMaxStages;
+// v as three bf16 parts that add up to it exactly (24 significant bits, cut toward zero so that
+// nothing overflows). NaN and Inf stay in the first part.
+__device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const uint32_t bits = __float_as_uint(v);
+    hi = bits & 0xFFFF0000u;
+    const float rest = v - __uint_as_float(hi);
+    mid = __float_as_uint(rest) & 0xFFFF0000u;
+    lo = __float_as_uint(rest - __uint_as_float(mid)) & 0xFFFF0000u;
+    if ((bits & 0x7F800000u) == 0x7F800000u) {
+        mid = lo = 0;
+        if (bits & 0x007FFFFFu) hi |= 0x00400000u;  // a NaN stays one
+    }
+}
+
+// First tile and number of tiles of block blk: the tiles cut evenly.
+__device__ __forceinline__ int block_tiles(const Plan& p, int blk, int& tile0) {
+    tile0 = (int)((long long)blk * p.tiles / p.nblk);
+    return (int)((long long)(blk + 1) * p.tiles / p.nblk) - tile0;
+}
+
+// TMA: rows of sign words are 16-byte aligned and come by TMA. F32: u is fp32.
+template <int NT, bool TMA, bool F32>
+__global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
+    mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap_less,
+               const __grid_constant__ GroupedCall c, const __grid_constant__ Plan p, unsigned* status) {
+    using S = Shape<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);  // for the 128-byte swizzle
+    const uint32_t ring = smem_addr(smem);
+    uint8_t* tail = smem + p.stages * p.stage_bytes;
+    const uint32_t full0 = smem_addr(tail), empty0 = full0 + 8 * kMaxStages;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 16 * kMaxStages);
+    float* red = reinterpret_cast<float*>(tail + kHead);  // [consumers][COLS][rp]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kw = c.K >> 5, runs = (kw + kRunWords - 1) / kRunWords;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(full0 + 8 * i, 32 * kProducers);
+            mbar_init(full0 + 8 * i, 32 * kProducers * (F32 && !TMA ? 2 : 1) + (TMA ? 1 : 0));
             mbar_init(empty0 + 8 * i, 4);
         }
         *abort_flag = 0;
         fence_barrier_init();
+        if (TMA) {
+            prefetch_tensormap(&wmap);
+            prefetch_tensormap(&wmap_less);
+        }
     }
     __syncthreads();
 
     UnitWalk walk;
     Unit u;
-    const int per = p.cols_pass / p.planes;  // slots of a unit
     int st = 0, phase = 0;
-    if (warp >= kConsumers) {
-        // ---- producers
-        const int tid = threadIdx.x - 32 * kConsumers;
+    auto advance = [&] {
+        if (++st == p.stages) st = 0, phase ^= 1;
+    };
+    if (warp >= S::CONSUMERS) {
+        // ---- producers: a thread copies the 16-byte chunk `tid` (8 k) of every column
+        constexpr int SLOTS = F32 ? (8 * NT) / 3 : 8 * NT;  // slots of a pass, at most
+        const int tid = threadIdx.x - 32 * S::CONSUMERS;
         bool stop = false;  // the same in all lanes of a warp
-        for (long long unit = blockIdx.x; !stop && walk.find<true>(c, per, p.nblk, unit, lane, u); unit += gridDim.x) {
-            const int e = u.e, slot0 = u.slot0, slots = u.slots, row0 = u.blk * R, cols = slots * p.planes;
-            const uint32_t* w0 = c.packed + ((long long)e * c.out + row0) * kw;
-            const int rows_left = c.out - row0;
+        int issued = 0;
+        for (long long unit = blockIdx.x; !stop && walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
+            int tile0;
+            const int h = block_tiles(p, u.blk, tile0), rows_left = c.out - 16 * tile0;
+            const char* src[SLOTS];  // this thread's chunk of run 0 of each slot's row of u, or null
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                src[i] = nullptr;
+                if (i < u.slots) {
+                    const long long row = c.rows ? (long long)__ldg(c.rows + u.slot0 + i) : u.slot0 + i;
+                    if (row >= 0 && row < c.tokens)
+                        src[i] = static_cast<const char*>(c.u) + (row * c.K + 8 * tid) * (F32 ? 4 : 2);
+                }
+            }
+            float4 ahead[F32 ? SLOTS : 1][2];
+            auto load = [&](int run) {
+                const bool in = run * kRunK + 8 * tid < c.K;
+#pragma unroll
+                for (int i = 0; i < SLOTS; ++i)
+                    if (i < u.slots) {
+                        const float4* q = reinterpret_cast<const float4*>(src[i] + (long long)run * kRunK * 4);
+                        const float4 zero = {0.f, 0.f, 0.f, 0.f};
+                        ahead[F32 ? i : 0][0] = in && src[i] ? __ldg(q) : zero;
+                        ahead[F32 ? i : 0][1] = in && src[i] ? __ldg(q + 1) : zero;
+                    }
+            };
+            if (F32) load(0);
             for (int run = 0; run < runs; ++run) {
-                const bool free = !*abort_flag && mbar_wait(empty0 + 8 * st, phase ^ 1, status);
+                const bool free = mbar_try_wait(empty0 + 8 * st, phase ^ 1) ||
+                                  (!*abort_flag && mbar_wait(empty0 + 8 * st, phase ^ 1, status));
                 if (!__all_sync(0xffffffffu, free)) {
                     *abort_flag = 1;
                     stop = true;
                     break;
                 }
-                const uint32_t a_st = ring + st * p.stage_bytes, u_st = a_st + R * 128;
-                const int word0 = run * kRunWords;
-                // sign words: piece x of row r goes to 16-byte chunk (x / 16) ^ (r % 8) of the row
-                constexpr int PIECES = 128 / VEC;
-                for (int i = tid; i < R * PIECES; i += 32 * kProducers) {
-                    const int r = i / PIECES, x = (i % PIECES) * (VEC / 4);
-                    const bool there = r < rows_left && word0 + x < kw &&
-                                       LQ_IN_BOUNDS(((long long)e * c.out + row0 + r) * kw + word0 + x + VEC / 4 - 1,
-                                                    (long long)c.experts * c.out * kw);
-                    const uint32_t dst = a_st + r * 128 + (((x >> 2) ^ (r & 7)) << 4) + (x & 3) * 4;
-                    const void* src = there ? w0 + (long long)r * kw + word0 + x : c.packed;
-                    if constexpr (VEC == 16)
-                        cp_async16(dst, src, there);
-                    else
-                        cp_async_small<VEC>(dst, src, there);
+                const uint32_t a_st = ring + st * p.stage_bytes, bar = full0 + 8 * st;
+                const uint32_t u_st = a_st + p.hmax * 2048 + tid * 16;
+                if (TMA) {
+                    if (warp == S::CONSUMERS && lane == 0) {
+                        mbar_arrive_expect_tx(bar, h * 2048);
+                        tma_load_2d(a_st, h == p.hmax ? &wmap : &wmap_less, run * kRunWords, u.e * c.out + 16 * tile0, bar);
+                    }
+                    __syncwarp();
+                } else {
+                    // word x of row r goes to 16-byte chunk (x / 4) ^ (r % 8) of the row, as TMA would put it
+                    const uint32_t* w0 = c.packed + ((long long)u.e * c.out + 16 * tile0) * kw + run * kRunWords;
+                    const int x = tid & 31;
+                    for (int r = tid >> 5; r < 16 * h; r += kProducers) {
+                        const bool there = r < rows_left && run * kRunWords + x < kw &&
+                                           LQ_IN_BOUNDS(((long long)u.e * c.out + 16 * tile0 + r) * kw + run * kRunWords + x,
+                                                        (long long)c.experts * c.out * kw);
+                        cp_async4(a_st + r * 128 + (((x >> 2) ^ (r & 7)) << 4) + (x & 3) * 4,
+                                  there ? w0 + (long long)r * kw + x : c.packed, there);
+                    }
                 }
-                // u rows of the columns
-                for (int i = tid; i < cols * (kRunK / 8); i += 32 * kProducers) {
-                    const int col = i >> 7, x = (i & 127) * 8;
-                    const int slot = slot0 + col / p.planes;
-                    long long row = c.rows ? (long long)__ldg(c.rows + slot) : slot;
-                    bool there = row >= 0 && row < c.tokens && run * kRunK + x < c.K;
-                    row = row * p.planes + col % p.planes;
-                    there = there && LQ_IN_BOUNDS(row * c.K + run * kRunK + x + 7, (long long)c.tokens * p.planes * c.K);
-                    const uint16_t* ub = static_cast<const uint16_t*>(c.u);
-                    cp_async16(u_st + col * kUPitch + x * 2, there ? ub + row * c.K + run * kRunK + x : ub, there);
+                if (F32) {
+                    float4 now[SLOTS][2];
+#pragma unroll
+                    for (int i = 0; i < SLOTS; ++i) now[i][0] = ahead[F32 ? i : 0][0], now[i][1] = ahead[F32 ? i : 0][1];
+                    if (run + 1 < runs) load(run + 1);
+#pragma unroll
+                    for (int i = 0; i < SLOTS; ++i)
+                        if (i < u.slots) {
+                            const float v[8] = {now[i][0].x, now[i][0].y, now[i][0].z, now[i][0].w,
+                                                now[i][1].x, now[i][1].y, now[i][1].z, now[i][1].w};
+                            uint32_t part[3][4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t a[3], b[3];
+                                split3(v[2 * j], a[0], a[1], a[2]);
+                                split3(v[2 * j + 1], b[0], b[1], b[2]);
+#pragma unroll
+                                for (int q = 0; q < 3; ++q) part[q][j] = __byte_perm(a[q], b[q], 0x7632);
+                            }
+#pragma unroll
+                            for (int q = 0; q < 3; ++q)
+                                sts128(u_st + (3 * i + q) * kUPitch, make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]));
+                        }
+                    mbar_arrive(bar);
+                } else {
+                    const bool in = run * kRunK + 8 * tid < c.K;
+#pragma unroll
+                    for (int i = 0; i < SLOTS; ++i)
+                        if (i < u.slots) {
+                            const bool there = in && src[i];
+                            cp_async16(u_st + i * kUPitch, there ? src[i] + (long long)run * kRunK * 2 : c.u, there);
+                        }
                 }
-                cp_async_arrive(full0 + 8 * st);
-                if (++st == p.stages) st = 0, phase ^= 1;
+                if (!F32 || !TMA) cp_async_arrive(bar);
+                ++issued;
+                advance();
             }
         }
         cp_async_wait_all();
+        if (TMA && warp == S::CONSUMERS)  // no TMA copy is in flight either: the last one of each stage has landed
+            for (int back = issued < p.stages ? issued : p.stages; back > 0; --back) {
+                const int at = issued - back;
+                mbar_wait(full0 + 8 * (at % p.stages), (at / p.stages) & 1, status);
+            }
         return;
     }
 
     // ---- consumers
     const int g = lane >> 2, t = lane & 3, quarter = warp & 3, group = warp >> 2;
     const uint32_t rot = t >= 2 ? 0x1032u : 0x3210u;
-    long long done = 0;  // runs before this unit, over all units
-    for (long long unit = blockIdx.x; walk.find<true>(c, per, p.nblk, unit, lane, u); unit += gridDim.x) {
-        const int e = u.e, slot0 = u.slot0, slots = u.slots, row0 = u.blk * R, cols = slots * p.planes;
-        float acc[H][NT][4];
+    int turn = 0;  // the group that takes the next run
+    for (long long unit = blockIdx.x; walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
+        int tile0;
+        const int h = block_tiles(p, u.blk, tile0), cols = u.slots * p.planes;
+        float acc[S::H][NT][4];
 #pragma unroll
-        for (int i = 0; i < H; ++i)
+        for (int i = 0; i < S::H; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.f;
         for (int run = 0; run < runs; ++run) {
-            const bool mine = ((done + run) & 1) == group;
-            if (mine) {
-                if (!*abort_flag && !mbar_wait(full0 + 8 * st, phase, status)) *abort_flag = 1;
+            if (turn == group) {
+                if (!mbar_try_wait(full0 + 8 * st, phase) && !*abort_flag && !mbar_wait(full0 + 8 * st, phase, status))
+                    *abort_flag = 1;
                 const uint32_t a_st = ring + st * p.stage_bytes;
-                const uint32_t u_st = a_st + R * 128 + quarter * 512 + t * 64 + (t >= 2 ? 32 : 0);
+                const uint32_t u_st = a_st + p.hmax * 2048 + quarter * 512 + t * 64 + (t >= 2 ? 32 : 0);
                 const uint32_t u_other = t >= 2 ? -32 : 32;
                 uint32_t b[NT][2][16];
 #pragma unroll
@@ -201,25 +300,26 @@ __global__ void __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant_
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int half = 0; half < 2; ++half) {
                             uint4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
                             if (col < cols) {
-                                const uint32_t at = u_st + col * kUPitch + x * 256 + h * 16;
+                                const uint32_t at = u_st + col * kUPitch + x * 256 + half * 16;
                                 lo = lds128(at);
                                 hi = lds128(at + u_other);
                             }
                             const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                b[n][x][8 * h + 2 * i] = __byte_perm(l[i], v[i], 0x5410);
-                                b[n][x][8 * h + 2 * i + 1] = __byte_perm(l[i], v[i], 0x7632);
+                                b[n][x][8 * half + 2 * i] = __byte_perm(l[i], v[i], 0x5410);
+                                b[n][x][8 * half + 2 * i + 1] = __byte_perm(l[i], v[i], 0x7632);
                             }
                         }
                 }
                 // row g of tile i: chunk 2 quarter + x, swizzled by the row; rows 8 apart share the swizzle
                 const uint32_t a_row = a_st + g * 128 + t * 4;
 #pragma unroll
-                for (int i = 0; i < H; ++i)
+                for (int i = 0; i < S::H; ++i) {
+                    if (i >= h) break;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t at = a_row + i * 2048 + (((2 * quarter + x) ^ g) << 4);
@@ -232,147 +332,136 @@ __global__ void __launch_bounds__(kThreads, 1) mma_kernel(const __grid_constant_
                             for (int n = 0; n < NT; ++n) mma_bf16(acc[i][n], a0, a1, a2, a3, b[n][x][j], b[n][x][j + 1]);
                         }
                     }
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
             }
-            if (++st == p.stages) st = 0, phase ^= 1;
+            if (++turn == S::GROUPS) turn = 0;
+            advance();
         }
-        done += runs;
 
         // ---- the warps' sums, in warp order
 #pragma unroll
-        for (int i = 0; i < H; ++i)
+        for (int i = 0; i < S::H; ++i) {
+            if (i >= h) break;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    red[(warp * COLS + 8 * n + 2 * t + (j & 1)) * RP + 16 * i + g + (j >> 1) * 8] = acc[i][n][j];
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+                    red[(warp * S::COLS + 8 * n + 2 * t + (j & 1)) * p.rp + 16 * i + g + (j >> 1) * 8] = acc[i][n][j];
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * S::CONSUMERS) : "memory");
         if (!*abort_flag) {
-            const int step = c.glu ? 2 : 1, per_col = R / step, width = c.glu ? c.out / 2 : c.out;
-            for (int x = threadIdx.x; x < slots * per_col; x += 32 * kConsumers) {
-                const int slot = x / per_col, r = (x - slot * per_col) * step;
-                if (row0 + r >= c.out) continue;
+            const int step = c.glu ? 2 : 1, per_col = 16 * h / step, width = c.glu ? c.out / 2 : c.out;
+            for (int x = threadIdx.x; x < u.slots * per_col; x += 32 * S::CONSUMERS) {
+                const int slot = x / per_col, r = (x - slot * per_col) * step, row = 16 * tile0 + r;
+                if (row >= c.out) continue;
                 float z[2] = {0.f, 0.f};
                 for (int q = 0; q < p.planes; ++q)
-                    for (int w = 0; w < kConsumers; ++w)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (h < step) z[h] += red[(w * COLS + slot * p.planes + q) * RP + r + h];
-                for (int h = 0; h < step; ++h) {
-                    const long long at = (long long)e * c.out + row0 + r + h;
-                    z[h] = __ldg(c.s + at) * z[h] + (c.bias ? __ldg(c.bias + at) : 0.f);
+                    for (int w = 0; w < S::CONSUMERS; ++w)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (k < step) z[k] += red[(w * S::COLS + slot * p.planes + q) * p.rp + r + k];
+                for (int k = 0; k < step; ++k) {
+                    const long long at = (long long)u.e * c.out + row + k;
+                    z[k] = __ldg(c.s + at) * z[k] + (c.bias ? __ldg(c.bias + at) : 0.f);
                 }
                 const float y = c.glu ? activate(z[0], c.act) * z[1] : activate(z[0], c.act);
-                const long long at = (long long)(slot0 + slot) * width + (row0 + r) / step;
+                const long long at = (long long)(u.slot0 + slot) * width + row / step;
                 if (LQ_IN_BOUNDS(at, (long long)c.n * width))
                     store_elem(c.o, at, c.o_bf16, c.residual ? y + load_elem(c.residual, at, c.o_bf16) : y);
             }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * S::CONSUMERS) : "memory");
     }
 }
 
-// fp32 u as three bf16 parts that add up to it exactly (24 significant bits, cut
-// toward zero so that nothing overflows): row 3 b + p of the planes is part p of row
-// b. NaN and Inf stay in the first part.
-__global__ void split_kernel(const float* __restrict__ u, long long count, int K, uint16_t* __restrict__ planes) {
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += (long long)gridDim.x * blockDim.x) {
-        const float v = __ldg(u + i);
-        const uint32_t bits = __float_as_uint(v);
-        uint32_t hi = bits & 0xFFFF0000u, mid = 0, lo = 0;
-        if ((bits & 0x7F800000u) != 0x7F800000u) {
-            const float rest = v - __uint_as_float(hi);
-            mid = __float_as_uint(rest) & 0xFFFF0000u;
-            lo = __float_as_uint(rest - __uint_as_float(mid));
-        } else if (bits & 0x007FFFFFu) {
-            hi |= 0x00400000u;  // a NaN stays one
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<EncodeTiledFn>(p)
+                   : nullptr;
+    }();
+    return fn;
+}
+
+template <int NT, bool TMA, bool F32>
+cudaError_t launch_as(const GroupedCall& c, const Plan& p, int h, unsigned* status, cudaStream_t st, int sms) {
+    CUtensorMap maps[2] = {};  // sign words of all experts in boxes of 16 h and 16 (h - 1) rows
+    if (TMA) {
+        EncodeTiledFn encode = encode_fn();
+        if (!encode) return cudaErrorNotSupported;
+        cuuint64_t gdim[2] = {(cuuint64_t)(c.K / 32), (cuuint64_t)c.experts * c.out};
+        cuuint64_t gstride[1] = {(cuuint64_t)c.K / 8};
+        cuuint32_t estride[2] = {1, 1};
+        for (int i = 0; i < 2; ++i) {
+            cuuint32_t box[2] = {(cuuint32_t)kRunWords, (cuuint32_t)(16 * (h - i > 0 ? h - i : 1))};
+            if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t*>(c.packed), gdim, gstride, box, estride,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
         }
-        const long long b = i / K, k = i - b * K;
-        planes[(3 * b) * K + k] = (uint16_t)(hi >> 16);
-        planes[(3 * b + 1) * K + k] = (uint16_t)(mid >> 16);
-        planes[(3 * b + 2) * K + k] = (uint16_t)(lo >> 16);
     }
-}
-
-template <int H, int NT, int VEC>
-cudaError_t launch_vec(const GroupedCall& c, const Plan& p, unsigned* status, cudaStream_t st, int sms) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(mma_kernel<H, NT, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+        cudaError_t e = cudaFuncSetAttribute(mma_kernel<NT, TMA, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(kSmemMax + 1024));
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    mma_kernel<H, NT, VEC><<<sms, kThreads, p.smem, st>>>(c, p, status);
+    mma_kernel<NT, TMA, F32><<<sms, Shape<NT>::THREADS, p.smem, st>>>(maps[0], maps[1], c, p, status);
     return cudaGetLastError();
 }
 
-template <int H, int NT>
-cudaError_t launch_h(const GroupedCall& c, Plan p, unsigned* status, cudaStream_t st, int sms) {
-    const size_t head = 512 + (size_t)kConsumers * 8 * NT * (16 * H + 4) * 4;
-    p.stage_bytes = 16 * H * 128 + (p.cols_cap * kUPitch + 127) / 128 * 128;
-    p.nblk = (c.out + 16 * H - 1) / (16 * H);
-    p.stages = (int)((kSmemMax - head) / p.stage_bytes);
-    p.stages = p.stages > kMaxStages ? kMaxStages : p.stages;
-    p.smem = head + (size_t)p.stages * p.stage_bytes;
-    const int kw = c.K >> 5;
-    if (kw % 4 == 0) return launch_vec<H, NT, 16>(c, p, status, st, sms);
-    if (kw % 2 == 0) return launch_vec<H, NT, 8>(c, p, status, st, sms);
-    return launch_vec<H, NT, 4>(c, p, status, st, sms);
+template <int NT>
+cudaError_t launch_nt(const GroupedCall& c, Plan p, int h, unsigned* status, cudaStream_t st, int sms) {
+    p.hmax = h;
+    p.rp = 16 * h + 4;
+    const size_t red = (size_t)Shape<NT>::CONSUMERS * Shape<NT>::COLS * p.rp * 4;
+    const int cols = (c.n < p.per ? c.n : p.per) * p.planes;
+    p.stage_bytes = (h * 2048 + cols * kUPitch + 1023) / 1024 * 1024;
+    const int fit = (int)((kSmemMax - kHead - red) / p.stage_bytes);
+    p.stages = fit > kMaxStages ? kMaxStages : fit;
+    p.smem = 1024 + (size_t)p.stages * p.stage_bytes + kHead + red;
+    const bool tma = c.K % 128 == 0;
+    if (c.u_bf16) return tma ? launch_as<NT, true, false>(c, p, h, status, st, sms) : launch_as<NT, false, false>(c, p, h, status, st, sms);
+    return tma ? launch_as<NT, true, true>(c, p, h, status, st, sms) : launch_as<NT, false, true>(c, p, h, status, st, sms);
 }
 
 }  // namespace
 
-size_t grouped_mma_workspace_size(int K, int n, bool u_bf16) {
-    return u_bf16 ? 0 : (size_t)3 * n * K * 2;
-}
-
-cudaError_t launch_grouped_mma(const GroupedCall& call, void* ws, unsigned* status, cudaStream_t st, int sms) {
-    GroupedCall c = call;
+cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
     Plan p{};
     p.planes = c.u_bf16 ? 1 : 3;
     for (int j = 0; j < 16; ++j) p.shift[j] = 1u << (15 - j);
-    if (!c.u_bf16) {
-        const long long count = (long long)c.tokens * c.K;
-        split_kernel<<<(int)((count + 255) / 256 < 4 * sms ? (count + 255) / 256 : 4 * sms), 256, 0, st>>>(
-            static_cast<const float*>(c.u), count, c.K, static_cast<uint16_t*>(ws));
-        c.u = ws;
-    }
-    // expected slots of an expert that has any: the pass width, 8 or 16 columns
+    // expected columns of an expert that has any: a pass of 8 or of 16
     const int active = c.n < c.experts ? c.n : c.experts;
-    const long long each = ((long long)c.n + active - 1) / active * p.planes;
-    const int nt = each > 8 ? 2 : 1;
-    p.cols_pass = 8 * nt / p.planes * p.planes;
-    p.cols_cap = (long long)c.n * p.planes < p.cols_pass ? c.n * p.planes : p.cols_pass;
+    const long long each = ((long long)c.n + active - 1) / active;
+    const int nt = each * p.planes > 8 ? 2 : 1;
+    p.per = 8 * nt / p.planes;
     // block height: rounds of blocks over the SMs times their length (a block's fixed cost is about one tile)
-    const long long tiles = (c.out + 15) / 16, passes = (each + p.cols_pass - 1) / p.cols_pass;
-    int best = 1;
+    p.tiles = (c.out + 15) / 16;
+    const long long passes = (each + p.per - 1) / p.per;
     long long best_cost = -1;
-    for (int h = 1; h <= (nt == 1 ? 8 : 6); ++h) {
-        if (nt == 2 && h == 5) continue;
-        const long long units = active * passes * ((tiles + h - 1) / h);
+    int best = 1;
+    for (int h = 1; h <= (nt == 1 ? Shape<1>::H : Shape<2>::H); ++h) {
+        const long long units = active * passes * ((p.tiles + h - 1) / h);
         const long long cost = (units + sms - 1) / sms * (h + 1);
         if (best_cost < 0 || cost < best_cost) best = h, best_cost = cost;
     }
-    if (nt == 1) switch (best) {
-        case 1: return launch_h<1, 1>(c, p, status, st, sms);
-        case 2: return launch_h<2, 1>(c, p, status, st, sms);
-        case 3: return launch_h<3, 1>(c, p, status, st, sms);
-        case 4: return launch_h<4, 1>(c, p, status, st, sms);
-        case 5: return launch_h<5, 1>(c, p, status, st, sms);
-        case 6: return launch_h<6, 1>(c, p, status, st, sms);
-        case 7: return launch_h<7, 1>(c, p, status, st, sms);
-        default: return launch_h<8, 1>(c, p, status, st, sms);
-    }
-    switch (best) {
-        case 1: return launch_h<1, 2>(c, p, status, st, sms);
-        case 2: return launch_h<2, 2>(c, p, status, st, sms);
-        case 3: return launch_h<3, 2>(c, p, status, st, sms);
-        case 4: return launch_h<4, 2>(c, p, status, st, sms);
-        default: return launch_h<6, 2>(c, p, status, st, sms);
-    }
+    p.nblk = (p.tiles + best - 1) / best;
+    const int h = (p.tiles + p.nblk - 1) / p.nblk;  // blocks have h or h - 1 tiles
+    return nt == 1 ? launch_nt<1>(c, p, h, status, st, sms) : launch_nt<2>(c, p, h, status, st, sms);
 }
 
 }  // namespace lq

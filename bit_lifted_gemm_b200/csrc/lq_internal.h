@@ -127,8 +127,7 @@ struct GroupedCall {
 size_t grouped_workspace_size(const GroupedCall& c);  // sizes and types of c alone
 cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st);
 // Its kernel for few rows per expert (lq_grouped_mma.cu), on `sms` CTAs.
-size_t grouped_mma_workspace_size(int K, int n, bool u_bf16);
-cudaError_t launch_grouped_mma(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st, int sms);
+cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms);
 // Its kernel for many rows per expert (lq_grouped_tc.cu): bf16 u, about `each` slots to an expert.
 size_t grouped_tc_workspace_size(int K, int n);  // used when rows are given
 cudaError_t launch_grouped_tc(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st, int sms, int each);
