@@ -18,8 +18,9 @@
 // warps form groups of four that take the runs in turn; the four warps of a group take a
 // quarter of the run each (8 words, 256 k) of all rows. A warp keeps its u fragments of the run in
 // registers while it walks the rows, so each sign word is expanded once and each u fragment
-// loaded once per 16 h rows. At the end of a block the warps' sums are added in warp
-// order through shared memory (the result does not depend on timing), and the epilogue runs.
+// loaded once per 16 h rows. At the end of a block the warps leave their sums in shared memory
+// and go on; four warps of their own add them in warp order (the result does not depend on
+// timing) and run the epilogue.
 //
 // Order of k. Thread (g, t) = (lane / 4, lane % 4) owns words t and 4 + t of the
 // warp's eight. Register j of a word holds bits j and j + 16 at the sign positions
@@ -46,15 +47,28 @@ constexpr int kProducers = 4;                // warps
 constexpr int kUPitch = kRunK * 2 + 16;      // bytes of one u row of a stage: 16 off a multiple of 32
 constexpr int kMaxStages = 16;
 constexpr size_t kSmemMax = 227 * 1024 - 2048;
-constexpr size_t kHead = 512;  // barriers
+constexpr size_t kHead = 512 + 1024;  // barriers, a block's scales and biases
 
 // H: tiles of 16 rows that a block may have. One n8 tile of columns leaves registers for three
-// groups of consumers (128 a thread), two n8 tiles for two groups (168).
+// groups of consumers, two n8 tiles for two. The block is launched with LAUNCH_REGS a thread, which the
+// consumers raise to CONSUMER_REGS from what the producers and the epilogue's warps give up:
+// (3 x 120 + 2 x 56 of 5 x 96, 2 x 168 + 2 x 88 of 4 x 128).
 template <int NT>
 struct Shape {
     static constexpr int COLS = 8 * NT, H = NT == 1 ? 8 : 6, GROUPS = NT == 1 ? 3 : 2;
-    static constexpr int CONSUMERS = 4 * GROUPS, THREADS = 32 * (CONSUMERS + kProducers);
+    static constexpr int CONSUMERS = 4 * GROUPS, PRODUCER = CONSUMERS, EPILOGUE = CONSUMERS + kProducers;
+    static constexpr int THREADS = 32 * (EPILOGUE + 4);
+    static constexpr int LAUNCH_REGS = NT == 1 ? 96 : 128, CONSUMER_REGS = NT == 1 ? 120 : 168, OTHER_REGS = NT == 1 ? 56 : 88;
+    static_assert(CONSUMERS * CONSUMER_REGS + 8 * OTHER_REGS <= (CONSUMERS + 8) * LAUNCH_REGS, "more registers than the block has");
 };
+template <int R>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -89,6 +103,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
 
 struct Plan {
     uint32_t shift[16];  // 2^(15 - j): kept from the compiler, so that it multiplies (see sign_pair)
@@ -140,7 +159,10 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     const uint32_t ring = smem_addr(smem);
     uint8_t* tail = smem + p.stages * p.stage_bytes;
     const uint32_t full0 = smem_addr(tail), empty0 = full0 + 8 * kMaxStages;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 16 * kMaxStages);
+    const uint32_t red_full = full0 + 16 * kMaxStages, red_empty = red_full + 8;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 16 * kMaxStages + 16);
+    float* scale = reinterpret_cast<float*>(tail + 512);  // [128], and the biases
+    float* shift = scale + 128;
     float* red = reinterpret_cast<float*>(tail + kHead);  // [consumers][COLS][rp]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kw = c.K >> 5, runs = (kw + kRunWords - 1) / kRunWords;
@@ -150,6 +172,8 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
             mbar_init(full0 + 8 * i, 32 * kProducers * (F32 && !TMA ? 2 : 1) + (TMA ? 1 : 0));
             mbar_init(empty0 + 8 * i, 4);
         }
+        mbar_init(red_full, S::CONSUMERS);
+        mbar_init(red_empty, 4);
         *abort_flag = 0;
         fence_barrier_init();
         if (TMA) {
@@ -165,10 +189,77 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     auto advance = [&] {
         if (++st == p.stages) st = 0, phase ^= 1;
     };
-    if (warp >= S::CONSUMERS) {
+    if (warp >= S::EPILOGUE) {
+        // ---- epilogue of a block, while the consumers are at the next one: the warps' sums in warp order
+        fewer_registers<S::OTHER_REGS>();
+        const int step = c.glu ? 2 : 1, width = c.glu ? c.out / 2 : c.out;
+        for (long long unit = blockIdx.x; walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
+            int tile0;
+            const int h = block_tiles(p, u.blk, tile0), per_col = 16 * h / step;
+            // the rows' scales and biases, one row to a thread, before the sums are there
+            const int tid = threadIdx.x - 32 * S::EPILOGUE;
+            if (tid < 16 * h) {
+                const int row = min(16 * tile0 + tid, c.out - 1);
+                const long long at = (long long)u.e * c.out + row;
+                scale[tid] = __ldg(c.s + at);
+                shift[tid] = c.bias ? __ldg(c.bias + at) : 0.f;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (!mbar_try_wait(red_full, phase) && !*abort_flag && !mbar_wait(red_full, phase, status)) *abort_flag = 1;
+            if (!*abort_flag) {
+                constexpr int MANY = 4;  // outputs of a thread at a time
+                const int count = u.slots * per_col;
+                for (int x0 = tid; x0 < count; x0 += 128 * MANY) {
+                    float y[MANY], res[MANY];
+                    long long at[MANY];
+#pragma unroll
+                    for (int m = 0; m < MANY; ++m) {
+                        const int x = x0 + 128 * m;
+                        const int slot = x / per_col, row = 16 * tile0 + (x - slot * per_col) * step;
+                        at[m] = x < count && row < c.out ? (long long)(u.slot0 + slot) * width + row / step : -1;
+                        res[m] = c.residual && at[m] >= 0 ? load_elem(c.residual, at[m], c.o_bf16) : 0.f;
+                    }
+#pragma unroll
+                    for (int m = 0; m < MANY; ++m) {
+                        const int x = x0 + 128 * m;
+                        if (x >= count) break;
+                        const int slot = x / per_col, r = (x - slot * per_col) * step;
+                        float z[2] = {0.f, 0.f};
+                        for (int q = 0; q < p.planes; ++q) {
+                            const float* sums = red + (slot * p.planes + q) * p.rp + r;
+                            if (c.glu) {
+#pragma unroll
+                                for (int w = 0; w < S::CONSUMERS; ++w) {
+                                    const float2 v = *reinterpret_cast<const float2*>(sums + w * S::COLS * p.rp);
+                                    z[0] += v.x, z[1] += v.y;
+                                }
+                            } else {
+#pragma unroll
+                                for (int w = 0; w < S::CONSUMERS; ++w) z[0] += sums[w * S::COLS * p.rp];
+                            }
+                        }
+                        z[0] = scale[r] * z[0] + shift[r];
+                        y[m] = activate(z[0], c.act);
+                        if (c.glu) y[m] *= scale[r + 1] * z[1] + shift[r + 1];
+                    }
+#pragma unroll
+                    for (int m = 0; m < MANY; ++m)
+                        if (at[m] >= 0 && LQ_IN_BOUNDS(at[m], (long long)c.n * width))
+                            store_elem(c.o, at[m], c.o_bf16, c.residual ? y[m] + res[m] : y[m]);
+                }
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // scale and shift are free again
+            __syncwarp();
+            if (lane == 0) mbar_arrive(red_empty);
+            phase ^= 1;
+        }
+        return;
+    }
+    if (warp >= S::PRODUCER) {
+        fewer_registers<S::OTHER_REGS>();
         // ---- producers: a thread copies the 16-byte chunk `tid` (8 k) of every column
         constexpr int SLOTS = F32 ? (8 * NT) / 3 : 8 * NT;  // slots of a pass, at most
-        const int tid = threadIdx.x - 32 * S::CONSUMERS;
+        const int tid = threadIdx.x - 32 * S::PRODUCER;
         bool stop = false;  // the same in all lanes of a warp
         int issued = 0;
         for (long long unit = blockIdx.x; !stop && walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
@@ -208,7 +299,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                 const uint32_t a_st = ring + st * p.stage_bytes, bar = full0 + 8 * st;
                 const uint32_t u_st = a_st + p.hmax * 2048 + tid * 16;
                 if (TMA) {
-                    if (warp == S::CONSUMERS && lane == 0) {
+                    if (warp == S::PRODUCER && lane == 0) {
                         mbar_arrive_expect_tx(bar, h * 2048);
                         tma_load_2d(a_st, h == p.hmax ? &wmap : &wmap_less, run * kRunWords, u.e * c.out + 16 * tile0, bar);
                     }
@@ -264,7 +355,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
             }
         }
         cp_async_wait_all();
-        if (TMA && warp == S::CONSUMERS)  // no TMA copy is in flight either: the last one of each stage has landed
+        if (TMA && warp == S::PRODUCER)  // no TMA copy is in flight either: the last one of each stage has landed
             for (int back = issued < p.stages ? issued : p.stages; back > 0; --back) {
                 const int at = issued - back;
                 mbar_wait(full0 + 8 * (at % p.stages), (at / p.stages) & 1, status);
@@ -273,6 +364,8 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     }
 
     // ---- consumers
+    more_registers<S::CONSUMER_REGS>();
+    int red_phase = 1;
     const int g = lane >> 2, t = lane & 3, quarter = warp & 3, group = warp >> 2;
     const uint32_t rot = t >= 2 ? 0x1032u : 0x3210u;
     int turn = 0;  // the group that takes the next run
@@ -317,21 +410,49 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                 }
                 // row g of tile i: chunk 2 quarter + x, swizzled by the row; rows 8 apart share the swizzle
                 const uint32_t a_row = a_st + g * 128 + t * 4;
+                // K tiles from tile i on, step by step of 128 k; the words of the next step are loaded ahead
+                auto load_words = [&](uint32_t (&to)[2][2], int i, int x) {
+                    const uint32_t at = a_row + i * 2048 + (((2 * quarter + x) ^ g) << 4);
 #pragma unroll
-                for (int i = 0; i < S::H; ++i) {
-                    if (i >= h) break;
+                    for (int k = 0; k < 2; ++k) to[k][0] = lds32(at + k * 2048), to[k][1] = lds32(at + k * 2048 + 1024);
+                };
+                uint32_t next[2][2];
+                auto tiles = [&](auto many, int i) {
+                    constexpr int K = decltype(many)::value;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint32_t at = a_row + i * 2048 + (((2 * quarter + x) ^ g) << 4);
-                        const uint32_t wl = __byte_perm(lds32(at), 0, rot), wh = __byte_perm(lds32(at + 1024), 0, rot);
+                        uint32_t w[K][2];
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            w[k][0] = __byte_perm(next[k][0], 0, rot), w[k][1] = __byte_perm(next[k][1], 0, rot);
+                        if (x == 0)
+                            load_words(next, i, 1);
+                        else if (i + 2 < S::H)
+                            load_words(next, i + 2, 0);
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const uint32_t a0 = sign_pair(wl, p, j), a1 = sign_pair(wh, p, j);
-                            const uint32_t a2 = sign_pair(wl, p, j + 1), a3 = sign_pair(wh, p, j + 1);
+                            uint32_t a[K][4];
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma_bf16(acc[i][n], a0, a1, a2, a3, b[n][x][j], b[n][x][j + 1]);
+                            for (int k = 0; k < K; ++k) {
+                                a[k][0] = sign_pair(w[k][0], p, j), a[k][1] = sign_pair(w[k][1], p, j);
+                                a[k][2] = sign_pair(w[k][0], p, j + 1), a[k][3] = sign_pair(w[k][1], p, j + 1);
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int k = 0; k < K; ++k)
+                                    mma_bf16(acc[i + k][n], a[k][0], a[k][1], a[k][2], a[k][3], b[n][x][j], b[n][x][j + 1]);
                         }
                     }
+                };
+                // two tiles at a time, so that two chains of accumulation overlap. The second may be past the
+                // block's (words that are in the stage, sums that are not used): a path for single tiles made
+                // blocks of odd height 3% faster and the others up to 10% slower.
+                load_words(next, 0, 0);
+#pragma unroll
+                for (int i = 0; i < S::H; i += 2) {
+                    if (i >= h) break;
+                    tiles(Int<2>(), i);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
@@ -340,7 +461,9 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
             advance();
         }
 
-        // ---- the warps' sums, in warp order
+        // ---- this warp's sums, once the epilogue has read those of the block before
+        if (!mbar_try_wait(red_empty, red_phase) && !*abort_flag && !mbar_wait(red_empty, red_phase, status)) *abort_flag = 1;
+        red_phase ^= 1;
 #pragma unroll
         for (int i = 0; i < S::H; ++i) {
             if (i >= h) break;
@@ -350,30 +473,8 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                 for (int j = 0; j < 4; ++j)
                     red[(warp * S::COLS + 8 * n + 2 * t + (j & 1)) * p.rp + 16 * i + g + (j >> 1) * 8] = acc[i][n][j];
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * S::CONSUMERS) : "memory");
-        if (!*abort_flag) {
-            const int step = c.glu ? 2 : 1, per_col = 16 * h / step, width = c.glu ? c.out / 2 : c.out;
-            for (int x = threadIdx.x; x < u.slots * per_col; x += 32 * S::CONSUMERS) {
-                const int slot = x / per_col, r = (x - slot * per_col) * step, row = 16 * tile0 + r;
-                if (row >= c.out) continue;
-                float z[2] = {0.f, 0.f};
-                for (int q = 0; q < p.planes; ++q)
-#pragma unroll
-                    for (int w = 0; w < S::CONSUMERS; ++w)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (k < step) z[k] += red[(w * S::COLS + slot * p.planes + q) * p.rp + r + k];
-                for (int k = 0; k < step; ++k) {
-                    const long long at = (long long)u.e * c.out + row + k;
-                    z[k] = __ldg(c.s + at) * z[k] + (c.bias ? __ldg(c.bias + at) : 0.f);
-                }
-                const float y = c.glu ? activate(z[0], c.act) * z[1] : activate(z[0], c.act);
-                const long long at = (long long)(u.slot0 + slot) * width + row / step;
-                if (LQ_IN_BOUNDS(at, (long long)c.n * width))
-                    store_elem(c.o, at, c.o_bf16, c.residual ? y + load_elem(c.residual, at, c.o_bf16) : y);
-            }
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * S::CONSUMERS) : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(red_full);
     }
 }
 
