@@ -11,6 +11,7 @@
 #include <initializer_list>
 
 #include "lq.h"
+#include "lq_decode.h"
 #include "lq_internal.h"
 
 namespace {
@@ -406,24 +407,22 @@ int lq_gemm(const uint32_t* packed, const float* s, int out, int K, const uint16
 
 namespace {
 
-// The checks and the launch that lq_gemm_epilogue, lq_gemv_epilogue and
-// lq_gemm_grouped share; c.n, c.tokens, c.experts and c.out are positive and K
-// is a valid lifted width.
-int grouped_call(const lq::GroupedCall& c, int o_dtype, int glu, void* workspace, size_t workspace_bytes,
-                 void* stream) {
-    if (!c.packed || !c.s || !c.u || !c.o || !workspace) return LQ_ERR_INVALID_ARG;
-    if (!all_aligned16({c.packed, c.s, c.u, c.rows, c.offsets, c.bias, c.residual, c.o})) return LQ_ERR_INVALID_ARG;
+// What the fused-epilogue calls check alike, c.n, c.tokens, c.experts and c.out being positive and K a valid lifted
+// width. `u_elem`: bytes of an element of u; `need`: workspace bytes. LQ_OK if the call may launch.
+int epilogue_checks(const lq::GroupedCall& c, const void* u, size_t u_elem, int o_dtype, int glu, void* workspace,
+                    size_t workspace_bytes, size_t need) {
+    if (!c.packed || !c.s || !u || !c.o || !workspace) return LQ_ERR_INVALID_ARG;
+    if (!all_aligned16({c.packed, c.s, u, c.rows, c.offsets, c.bias, c.residual, c.o})) return LQ_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LQ_ERR_INVALID_ARG;
     if (o_dtype != LQ_F32 && o_dtype != LQ_BF16) return LQ_ERR_INVALID_ARG;
     if (c.act < LQ_ACT_NONE || c.act > LQ_ACT_SILU || (glu != 0 && glu != 1)) return LQ_ERR_INVALID_ARG;
     if (glu && c.out % 2 != 0) return LQ_ERR_INVALID_ARG;
-    const size_t need = lq::grouped_workspace_size(c);
-    if (workspace_bytes < need) return LQ_ERR_INVALID_ARG;
+    if (need == 0 || workspace_bytes < need) return LQ_ERR_INVALID_ARG;
     const long long rows_w = (long long)c.experts * c.out, width = glu ? c.out / 2 : c.out;
     const size_t oe = c.o_bf16 ? 2 : 4;
     if (aliased({{c.packed, nbytes(rows_w * (c.K / 32), 4), false},
                  {c.s, nbytes(rows_w, 4), false},
-                 {c.u, nbytes((long long)c.tokens * c.K, c.u_bf16 ? 2 : 4), false},
+                 {u, nbytes((long long)c.tokens * c.K, u_elem), false},
                  {c.rows, nbytes(c.n, 4), false},
                  {c.offsets, nbytes(c.experts + 1, 4), false},
                  {c.bias, nbytes(rows_w, 4), false},
@@ -435,8 +434,15 @@ int grouped_call(const lq::GroupedCall& c, int o_dtype, int glu, void* workspace
     const int sm = is_sm100();
     if (sm < 0) return LQ_ERR_CUDA;
     if (sm == 0) return LQ_ERR_UNSUPPORTED;
-    if (!all_on_current_device({c.packed, c.s, c.u, c.rows, c.offsets, c.bias, c.residual, c.o, workspace}))
+    if (!all_on_current_device({c.packed, c.s, u, c.rows, c.offsets, c.bias, c.residual, c.o, workspace}))
         return LQ_ERR_INVALID_ARG;
+    return LQ_OK;
+}
+
+int grouped_call(const lq::GroupedCall& c, int o_dtype, int glu, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    const int rc = epilogue_checks(c, c.u, 2, o_dtype, glu, workspace, workspace_bytes, lq::grouped_workspace_size(c));
+    if (rc != LQ_OK) return rc;
     int err = LQ_OK;
     unsigned* status = status_word(&err);
     if (!status) return err;
@@ -444,11 +450,33 @@ int grouped_call(const lq::GroupedCall& c, int o_dtype, int glu, void* workspace
 }
 
 // A call of one layer on all its rows.
-lq::GroupedCall layer_call(const uint32_t* packed, const float* s, int out, int K, const void* u, bool u_bf16,
-                           int tokens, const float* bias, int act, int glu, const void* residual, void* o,
-                           int o_dtype) {
-    return lq::GroupedCall{packed, s,    1,   out,      K,        u, u_bf16, tokens, nullptr, nullptr, tokens,
-                           bias,   act, glu != 0, residual, o, o_dtype == LQ_BF16};
+lq::GroupedCall layer_call(const uint32_t* packed, const float* s, int out, int K, const uint16_t* u, int tokens,
+                           const float* bias, int act, int glu, const void* residual, void* o, int o_dtype) {
+    lq::GroupedCall c{};
+    c.packed = packed;
+    c.s = s;
+    c.experts = 1;
+    c.out = out;
+    c.K = K;
+    c.u = u;
+    c.tokens = c.n = tokens;
+    c.bias = bias;
+    c.act = act;
+    c.glu = glu != 0;
+    c.residual = residual;
+    c.o = o;
+    c.o_bf16 = o_dtype == LQ_BF16;
+    return c;
+}
+
+// Sizes alone, for the workspace of a call.
+lq::GroupedCall sized_call(int experts, int out, int K, int n) {
+    lq::GroupedCall c{};
+    c.experts = experts;
+    c.out = out;
+    c.K = K;
+    c.tokens = c.n = n;
+    return c;
 }
 
 bool layer_sizes_ok(int out, int K) { return out >= 1 && K >= 32 && K % 32 == 0; }
@@ -466,37 +494,41 @@ extern "C" {
 
 size_t lq_gemm_epilogue_workspace_size(int out, int K, int tokens) {
     if (!layer_sizes_ok(out, K) || tokens < 1) return 0;
-    return lq::grouped_workspace_size(
-        layer_call(nullptr, nullptr, out, K, nullptr, true, tokens, nullptr, 0, 0, nullptr, nullptr, LQ_F32));
+    return lq::grouped_workspace_size(sized_call(1, out, K, tokens));
 }
 
 int lq_gemm_epilogue(const uint32_t* packed, const float* s, int out, int K, const uint16_t* u_bf16, int tokens,
                      const float* bias, int act, int glu, const void* residual, void* o, int o_dtype, void* workspace,
                      size_t workspace_bytes, void* stream) {
     if (!layer_sizes_ok(out, K) || tokens < 1) return LQ_ERR_INVALID_ARG;
-    return grouped_call(layer_call(packed, s, out, K, u_bf16, true, tokens, bias, act, glu, residual, o, o_dtype),
+    return grouped_call(layer_call(packed, s, out, K, u_bf16, tokens, bias, act, glu, residual, o, o_dtype),
                         o_dtype, glu, workspace, workspace_bytes, stream);
 }
 
 size_t lq_gemv_epilogue_workspace_size(int out, int K, int batch) {
     if (!layer_sizes_ok(out, K) || batch < 1 || batch > 16) return 0;
-    return lq::grouped_workspace_size(
-        layer_call(nullptr, nullptr, out, K, nullptr, false, batch, nullptr, 0, 0, nullptr, nullptr, LQ_F32));
+    return lq::gemv_epilogue_workspace_size(out, K, batch);
 }
 
 int lq_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K, const float* u, int batch,
                      const float* bias, int act, int glu, const void* residual, void* o, int o_dtype, void* workspace,
                      size_t workspace_bytes, void* stream) {
     if (!layer_sizes_ok(out, K) || batch < 1 || batch > 16) return LQ_ERR_INVALID_ARG;
-    return grouped_call(layer_call(packed, s, out, K, u, false, batch, bias, act, glu, residual, o, o_dtype), o_dtype,
-                        glu, workspace, workspace_bytes, stream);
+    const lq::GroupedCall c = layer_call(packed, s, out, K, nullptr, batch, bias, act, glu, residual, o, o_dtype);
+    const int rc = epilogue_checks(c, u, 4, o_dtype, glu, workspace, workspace_bytes,
+                                   lq::gemv_epilogue_workspace_size(out, K, batch));
+    if (rc != LQ_OK) return rc;
+    int err = LQ_OK;
+    unsigned* status = status_word(&err);
+    if (!status) return err;
+    const lq::DecodeEpilogue epi{bias, residual, o, nullptr, act, c.glu, c.o_bf16};
+    return from_cuda(lq::launch_gemv_epilogue(packed, s, out, K, u, batch, epi, workspace, status,
+                                              static_cast<cudaStream_t>(stream)));
 }
 
 size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n) {
     if (!grouped_sizes_ok(experts, out, K, n)) return 0;
-    lq::GroupedCall c =
-        layer_call(nullptr, nullptr, out, K, nullptr, true, n, nullptr, 0, 0, nullptr, nullptr, LQ_F32);
-    c.experts = experts;
+    lq::GroupedCall c = sized_call(experts, out, K, n);
     static const int some_offsets = 0;  // that there are offsets counts, not where
     c.offsets = &some_offsets;
     return lq::grouped_workspace_size(c);
@@ -507,7 +539,7 @@ int lq_gemm_grouped(const uint32_t* packed, const float* s, int experts, int out
                     void* o, int o_dtype, void* workspace, size_t workspace_bytes, void* stream) {
     if (!grouped_sizes_ok(experts, out, K, n) || tokens < 1 || !offsets) return LQ_ERR_INVALID_ARG;
     if (!rows && tokens < n) return LQ_ERR_INVALID_ARG;
-    lq::GroupedCall c = layer_call(packed, s, out, K, u_bf16, true, tokens, bias, act, glu, nullptr, o, o_dtype);
+    lq::GroupedCall c = layer_call(packed, s, out, K, u_bf16, tokens, bias, act, glu, nullptr, o, o_dtype);
     c.experts = experts;
     c.rows = rows;
     c.offsets = offsets;

@@ -92,6 +92,19 @@ struct DecodePlan {
     size_t off_hdr, off_steps, off_planes, off_count, off_slots, bytes;
 };
 
+// The fused epilogue of lq_gemv_epilogue, in place of plain stores of s[r] * acc:
+//   z = s[r] acc + bias[r]; o = act(z) + residual, or on row pairs act(z[2i]) z[2i+1] + residual.
+// `sums` ([batch][out] fp32 scratch) holds z between the launches of a K that
+// takes several; it is not touched otherwise.
+struct DecodeEpilogue {
+    const float* bias;     // [out] or NULL
+    const void* residual;  // [batch][width] in o's type, or NULL
+    void* o;               // [batch][width], width = glu ? out / 2 : out
+    float* sums;
+    int act;
+    bool glu, o_bf16;
+};
+
 // Host: the plan for (out, K, batch); .bytes == 0 if no plan fits.
 DecodePlan make_decode_plan(int out, int K, int batch);
 

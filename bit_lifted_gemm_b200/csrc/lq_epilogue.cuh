@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "lq.h"
+#include "lq_decode.h"
 
 namespace lq {
 
@@ -75,6 +76,21 @@ __device__ __forceinline__ void store_elem(void* p, long long i, bool bf16, floa
         static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
     else
         static_cast<float*>(p)[i] = v;
+}
+
+// The decode kernels' epilogue of one element: z of weight row r (scale applied, no bias yet) of column
+// c. Called by the lanes of rows 2i and 2i + 1 together, which are neighbours, when gated.
+__device__ __forceinline__ void finish_elem(const DecodeEpilogue& e, int out, int c, int r, float z, int lane) {
+    if (e.bias) z += __ldg(e.bias + r);
+    if (e.glu) {
+        const float other = __shfl_xor_sync(3u << (lane & 30), z, 1);
+        if (r & 1) return;
+        z = activate(z, e.act) * other;
+    } else {
+        z = activate(z, e.act);
+    }
+    const long long at = e.glu ? (long long)c * (out / 2) + r / 2 : (long long)c * out + r;
+    store_elem(e.o, at, e.o_bf16, e.residual ? z + load_elem(e.residual, at, e.o_bf16) : z);
 }
 
 }  // namespace lq

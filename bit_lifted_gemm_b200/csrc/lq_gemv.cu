@@ -60,6 +60,7 @@
 #include <cstring>
 
 #include "lq_decode.h"
+#include "lq_epilogue.cuh"
 #include "lq_internal.h"
 #include "lq_sm100.cuh"
 
@@ -178,6 +179,8 @@ struct GemvArgs {
     int pitch;        // chunks per shared-memory digit plane
     unsigned image_bytes;
     int accumulate;   // 1: o += this launch's result
+    int last;         // 1: no launch over K follows for these columns
+    DecodeEpilogue epi;
 };
 
 // Shared-memory carve-up (offsets from a 1024-byte-aligned base).
@@ -203,7 +206,8 @@ __host__ __device__ inline Layout gemv_layout(int ts, int stages, bool tma, bool
 
 // TS: steps per ring tile (2 with the 3-D weight map, else 1); STAGES: ring
 // depth; TMA: weights through the rings (else guarded register loads).
-template <int TS, int STAGES, bool TMA, bool USTAGE>
+// EPI: the epilogue of lq_gemv_epilogue in place of the plain stores of o.
+template <int TS, int STAGES, bool TMA, bool USTAGE, bool EPI>
 __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift beside it
     gemv_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap umap,
                 const GemvArgs p) {
@@ -643,6 +647,15 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
         } else {
             res = __int_as_float(0x7fc00000);
         }
+        if constexpr (EPI) {
+            float* part = p.epi.sums + (long long)(p.c0 + c) * p.out + m;
+            if (p.accumulate) res += *part;
+            if (p.last)
+                finish_elem(p.epi, p.out, p.c0 + c, m, res, lane);
+            else
+                *part = res;
+            continue;
+        }
         float* outp = p.o + (long long)(p.c0 + c) * p.out + m;
         *outp = p.accumulate ? *outp + res : res;
     }
@@ -727,10 +740,10 @@ bool plan_mma(DecodePlan& pl) {
     return false;  // the CTA's row partials (maxgroups) are too many
 }
 
-template <int TS, int STAGES, bool TMA, bool USTAGE>
+template <int TS, int STAGES, bool TMA, bool USTAGE, bool EPI>
 cudaError_t launch_kernel(const CUtensorMap& wmap, const CUtensorMap& umap, const GemvArgs& p, const DecodePlan& pl,
                           cudaStream_t st) {
-    auto kern = gemv_kernel<TS, STAGES, TMA, USTAGE>;
+    auto kern = gemv_kernel<TS, STAGES, TMA, USTAGE, EPI>;
     static size_t granted[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -752,24 +765,25 @@ cudaError_t launch_kernel(const CUtensorMap& wmap, const CUtensorMap& umap, cons
     return cudaLaunchKernelEx(&cfg, kern, wmap, umap, p);
 }
 
-template <bool US>
+template <bool US, bool EPI>
 cudaError_t launch_planned_us(const CUtensorMap& wmap, const CUtensorMap& umap, const GemvArgs& p,
                               const DecodePlan& pl, cudaStream_t st) {
     if (pl.ts == 2)
-        return pl.stages == 4 ? launch_kernel<2, 4, true, US>(wmap, umap, p, pl, st)
-                              : launch_kernel<2, 2, true, US>(wmap, umap, p, pl, st);
-    return pl.stages == 8 ? launch_kernel<1, 8, true, US>(wmap, umap, p, pl, st)
-                          : launch_kernel<1, 4, true, US>(wmap, umap, p, pl, st);
+        return pl.stages == 4 ? launch_kernel<2, 4, true, US, EPI>(wmap, umap, p, pl, st)
+                              : launch_kernel<2, 2, true, US, EPI>(wmap, umap, p, pl, st);
+    return pl.stages == 8 ? launch_kernel<1, 8, true, US, EPI>(wmap, umap, p, pl, st)
+                          : launch_kernel<1, 4, true, US, EPI>(wmap, umap, p, pl, st);
 }
 
+template <bool EPI>
 cudaError_t launch_planned(const CUtensorMap& wmap, const CUtensorMap& umap, bool ustage, const GemvArgs& p,
                            const DecodePlan& pl, cudaStream_t st) {
-    if (!pl.tma) return launch_kernel<1, 4, false, false>(wmap, umap, p, pl, st);
-    return ustage ? launch_planned_us<true>(wmap, umap, p, pl, st) : launch_planned_us<false>(wmap, umap, p, pl, st);
+    if (!pl.tma) return launch_kernel<1, 4, false, false, EPI>(wmap, umap, p, pl, st);
+    return ustage ? launch_planned_us<true, EPI>(wmap, umap, p, pl, st) : launch_planned_us<false, EPI>(wmap, umap, p, pl, st);
 }
 
 cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan& pl, const float* u, float* o,
-                       unsigned* status, cudaStream_t st) {
+                       const DecodeEpilogue* epi, unsigned* status, cudaStream_t st) {
     const int out = pl.out, kw = pl.kw;
     CUtensorMap wmap, umap;
     memset(&wmap, 0, sizeof(wmap));
@@ -832,7 +846,10 @@ cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan&
             p.pitch = pl.pitch;
             p.image_bytes = (unsigned)pl.image_bytes;
             p.accumulate = chunk > 0;
-            cudaError_t e = launch_planned(wmap, umap, ustage, p, pl, st);
+            p.last = chunk + 1 == pl.nchunk;
+            p.epi = epi ? *epi : DecodeEpilogue{};
+            cudaError_t e = epi ? launch_planned<true>(wmap, umap, ustage, p, pl, st)
+                                : launch_planned<false>(wmap, umap, ustage, p, pl, st);
             if (e != cudaSuccess) return e;
         }
     }
@@ -887,20 +904,43 @@ DecodePlan make_decode_plan(int out, int K, int batch) {
 
 size_t gemv_workspace_size(int out, int K, int batch) { return make_decode_plan(out, K, batch).bytes; }
 
-cudaError_t launch_gemv(const uint32_t* packed, const float* s, int out, int K, const float* u, int batch, float* o,
-                        void* ws, unsigned* status, cudaStream_t st) {
-    const DecodePlan pl = make_decode_plan(out, K, batch);
+namespace {
+
+cudaError_t launch_decode(const DecodePlan& pl, const uint32_t* packed, const float* s, const float* u, float* o,
+                          const DecodeEpilogue* epi, void* ws, unsigned* status, cudaStream_t st) {
     if (pl.bytes == 0) return cudaErrorInvalidValue;
     uint8_t* w = static_cast<uint8_t*>(ws);
     cudaError_t e;
     if (pl.tc) {
         e = launch_quant_mx(u, pl, w, st);
-        if (e == cudaSuccess) e = launch_gemv_tc(packed, s, pl, o, w, status, st);
+        if (e == cudaSuccess) e = launch_gemv_tc(packed, s, pl, o, epi, w, status, st);
     } else {
-        e = launch_mma(packed, s, pl, u, o, status, st);
+        e = launch_mma(packed, s, pl, u, o, epi, status, st);
     }
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+// The scratch of the sums between launches over K follows the plan's own workspace.
+size_t sums_bytes(const DecodePlan& pl) { return !pl.tc && pl.nchunk > 1 ? align256((size_t)pl.batch * pl.out * 4) : 0; }
+
+}  // namespace
+
+cudaError_t launch_gemv(const uint32_t* packed, const float* s, int out, int K, const float* u, int batch, float* o,
+                        void* ws, unsigned* status, cudaStream_t st) {
+    return launch_decode(make_decode_plan(out, K, batch), packed, s, u, o, nullptr, ws, status, st);
+}
+
+size_t gemv_epilogue_workspace_size(int out, int K, int batch) {
+    const DecodePlan pl = make_decode_plan(out, K, batch);
+    return pl.bytes ? pl.bytes + sums_bytes(pl) : 0;
+}
+
+cudaError_t launch_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K, const float* u, int batch,
+                                 DecodeEpilogue epi, void* ws, unsigned* status, cudaStream_t st) {
+    const DecodePlan pl = make_decode_plan(out, K, batch);
+    epi.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.bytes);
+    return launch_decode(pl, packed, s, u, nullptr, &epi, ws, status, st);
 }
 
 cudaError_t launch_lift_gemv(const void* a, bool a_bf16, int batch, int in, const float* tinv, int tblk,

@@ -49,6 +49,7 @@
 #include <cstring>
 
 #include "lq_decode.h"
+#include "lq_epilogue.cuh"
 #include "lq_internal.h"
 #include "lq_sm100.cuh"
 
@@ -79,6 +80,7 @@ struct TcArgs {
     unsigned* status;
     long long units;       // (group, sub-stage) units
     int out, kw, batch, bpad, N, nq, nqp, groups, nsub, maxcontrib, nacc, nss, nsa;
+    DecodeEpilogue epi;
 };
 
 struct Smem {
@@ -249,7 +251,8 @@ struct Ring {
     }
 };
 
-template <int MT>
+// EPI: the epilogue of lq_gemv_epilogue in place of the plain stores of o.
+template <int MT, bool EPI>
 __global__ void __launch_bounds__(tc_threads(MT), 1)
     gemv_tc_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap bmap,
                    const __grid_constant__ CUtensorMap dmap, const __grid_constant__ CUtensorMap smap,
@@ -584,7 +587,10 @@ __global__ void __launch_bounds__(tc_threads(MT), 1)
                     } else {
                         res = __int_as_float(0x7fc00000);
                     }
-                    p.o[(size_t)c * p.out + r] = res;
+                    if constexpr (EPI)
+                        finish_elem(p.epi, p.out, c, (int)r, res, lane);
+                    else
+                        p.o[(size_t)c * p.out + r] = res;
                 }
             };
             // ---- drain tile by tile: sum the planes of each column (plane p =
@@ -755,8 +761,8 @@ size_t tc_slot_bytes(const DecodePlan& p) {
     return p.tc_maxcontrib > 1 ? (size_t)p.tc_groups * p.tc_maxcontrib * p.batch * (128 * p.tc_mt) * sizeof(double) : 0;
 }
 
-cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodePlan& pl, float* o, uint8_t* ws,
-                           unsigned* status, cudaStream_t st) {
+cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodePlan& pl, float* o,
+                           const DecodeEpilogue* epi, uint8_t* ws, unsigned* status, cudaStream_t st) {
     EncodeTiledFn encode = encode_fn_tc();
     if (!encode) return cudaErrorNotSupported;
     CUtensorMap wmap, bmap, dmap, smap;
@@ -823,11 +829,14 @@ cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodeP
     a.nss = pl.tc_nss;
     a.nsa = pl.tc_nsa;
 
-    auto kern = pl.tc_mt == 4 ? gemv_tc_kernel<4> : gemv_tc_kernel<2>;
-    static size_t granted[2][64] = {};
+    a.epi = epi ? *epi : DecodeEpilogue{};
+
+    auto kern = epi ? (pl.tc_mt == 4 ? gemv_tc_kernel<4, true> : gemv_tc_kernel<2, true>)
+                    : (pl.tc_mt == 4 ? gemv_tc_kernel<4, false> : gemv_tc_kernel<2, false>);
+    static size_t granted[4][64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
-    const int ki = pl.tc_mt == 4 ? 1 : 0;
+    const int ki = (pl.tc_mt == 4 ? 1 : 0) + (epi ? 2 : 0);
     if (dev >= 64 || granted[ki][dev] < pl.tc_smem) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.tc_smem);
         if (e != cudaSuccess) return e;

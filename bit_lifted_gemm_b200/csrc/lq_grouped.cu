@@ -1,5 +1,5 @@
 // Routing of the products grouped by expert with the fused epilogue (lq_gemm_grouped;
-// lq_gemm_epilogue and lq_gemv_epilogue are its one-expert case):
+// lq_gemm_epilogue is its one-expert case):
 //
 //   z[i][r] = s_e[r] sum_k sigma_e[r][k] u[rows[i]][k] + bias_e[r],  offsets[e] <= i < offsets[e+1]
 //   o[i][r] = act(z[i][r]) + residual[i][r], or gated
@@ -19,7 +19,7 @@ int slots_each(const GroupedCall& c) {
     const int active = c.n < c.experts ? c.n : c.experts;
     return (int)(((long long)c.n + active - 1) / active);
 }
-bool few_rows(const GroupedCall& c) { return !c.u_bf16 || slots_each(c) <= 32; }
+bool few_rows(const GroupedCall& c) { return slots_each(c) <= 32; }
 
 }  // namespace
 

@@ -7,15 +7,15 @@
 // so the contraction is arranged around them: signs become the A operand of
 // mma.sync m16n8k16 (bf16, fp32 accumulate), 16 weight rows by 16 k, and rows of u
 // are its columns. +-1 and u are exact in bf16, so only the fp32 sums round; NaN and Inf
-// propagate as IEEE sums do. An fp32 u takes three columns, bf16 parts that add up to it.
+// propagate as IEEE sums do.
 //
 // A block is up to H tiles of 16 weight rows by one pass of one expert; blocks go round the
 // CTAs (one per SM). K is walked in runs of 1024 (32 sign words) through a ring of
 // shared-memory stages. Four producer warps fill them: one thread loads the block's
 // words of the run [16 h][32] by TMA (128-byte swizzle; 4-byte cp.async in the same layout
 // where rows of words are not 16-byte aligned), all of them copy the run's slice of u's
-// rows [cols][1024] with cp.async, zeros past K, or split fp32 rows on the way. The consumer
-// warps form groups of four that take the runs in turn; the four warps of a group take a
+// rows [cols][1024] with cp.async, zeros past K. The consumer warps
+// form groups of four that take the runs in turn; the four warps of a group take a
 // quarter of the run each (8 words, 256 k) of all rows. A warp keeps its u fragments of the run in
 // registers while it walks the rows, so each sign word is expanded once and each u fragment
 // loaded once per 16 h rows. At the end of a block the warps leave their sums in shared memory
@@ -100,10 +100,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 template <int V>
 struct Int {
     static constexpr int value = V;
@@ -112,7 +108,7 @@ struct Int {
 struct Plan {
     uint32_t shift[16];  // 2^(15 - j): kept from the compiler, so that it multiplies (see sign_pair)
     int stages, stage_bytes, rp;    // rp: pitch of a column of the warps' sums, in floats
-    int per, planes;                // slots of a pass, columns of a slot
+    int per;                        // slots of a pass: a column each
     int nblk, tiles, hmax;          // blocks and tiles of an expert's rows; a block has hmax tiles or one less
     size_t smem;
 };
@@ -128,28 +124,14 @@ __device__ __forceinline__ uint32_t sign_pair(uint32_t w, const Plan& p, int j) 
     return r;
 }
 
-// v as three bf16 parts that add up to it exactly (24 significant bits, cut toward zero so that
-// nothing overflows). NaN and Inf stay in the first part.
-__device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    const uint32_t bits = __float_as_uint(v);
-    hi = bits & 0xFFFF0000u;
-    const float rest = v - __uint_as_float(hi);
-    mid = __float_as_uint(rest) & 0xFFFF0000u;
-    lo = __float_as_uint(rest - __uint_as_float(mid)) & 0xFFFF0000u;
-    if ((bits & 0x7F800000u) == 0x7F800000u) {
-        mid = lo = 0;
-        if (bits & 0x007FFFFFu) hi |= 0x00400000u;  // a NaN stays one
-    }
-}
-
 // First tile and number of tiles of block blk: the tiles cut evenly.
 __device__ __forceinline__ int block_tiles(const Plan& p, int blk, int& tile0) {
     tile0 = (int)((long long)blk * p.tiles / p.nblk);
     return (int)((long long)(blk + 1) * p.tiles / p.nblk) - tile0;
 }
 
-// TMA: rows of sign words are 16-byte aligned and come by TMA. F32: u is fp32.
-template <int NT, bool TMA, bool F32>
+// TMA: rows of sign words are 16-byte aligned and come by TMA.
+template <int NT, bool TMA>
 __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap_less,
                const __grid_constant__ GroupedCall c, const __grid_constant__ Plan p, unsigned* status) {
@@ -169,7 +151,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(full0 + 8 * i, 32 * kProducers * (F32 && !TMA ? 2 : 1) + (TMA ? 1 : 0));
+            mbar_init(full0 + 8 * i, 32 * kProducers + (TMA ? 1 : 0));
             mbar_init(empty0 + 8 * i, 4);
         }
         mbar_init(red_full, S::CONSUMERS);
@@ -225,18 +207,16 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                         if (x >= count) break;
                         const int slot = x / per_col, r = (x - slot * per_col) * step;
                         float z[2] = {0.f, 0.f};
-                        for (int q = 0; q < p.planes; ++q) {
-                            const float* sums = red + (slot * p.planes + q) * p.rp + r;
-                            if (c.glu) {
+                        const float* sums = red + slot * p.rp + r;
+                        if (c.glu) {
 #pragma unroll
-                                for (int w = 0; w < S::CONSUMERS; ++w) {
-                                    const float2 v = *reinterpret_cast<const float2*>(sums + w * S::COLS * p.rp);
-                                    z[0] += v.x, z[1] += v.y;
-                                }
-                            } else {
-#pragma unroll
-                                for (int w = 0; w < S::CONSUMERS; ++w) z[0] += sums[w * S::COLS * p.rp];
+                            for (int w = 0; w < S::CONSUMERS; ++w) {
+                                const float2 v = *reinterpret_cast<const float2*>(sums + w * S::COLS * p.rp);
+                                z[0] += v.x, z[1] += v.y;
                             }
+                        } else {
+#pragma unroll
+                            for (int w = 0; w < S::CONSUMERS; ++w) z[0] += sums[w * S::COLS * p.rp];
                         }
                         z[0] = scale[r] * z[0] + shift[r];
                         y[m] = activate(z[0], c.act);
@@ -258,36 +238,22 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     if (warp >= S::PRODUCER) {
         fewer_registers<S::OTHER_REGS>();
         // ---- producers: a thread copies the 16-byte chunk `tid` (8 k) of every column
-        constexpr int SLOTS = F32 ? (8 * NT) / 3 : 8 * NT;  // slots of a pass, at most
         const int tid = threadIdx.x - 32 * S::PRODUCER;
         bool stop = false;  // the same in all lanes of a warp
         int issued = 0;
         for (long long unit = blockIdx.x; !stop && walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
             int tile0;
             const int h = block_tiles(p, u.blk, tile0), rows_left = c.out - 16 * tile0;
-            const char* src[SLOTS];  // this thread's chunk of run 0 of each slot's row of u, or null
+            const uint16_t* src[S::COLS];  // this thread's chunk of run 0 of each slot's row of u, or null
 #pragma unroll
-            for (int i = 0; i < SLOTS; ++i) {
+            for (int i = 0; i < S::COLS; ++i) {
                 src[i] = nullptr;
                 if (i < u.slots) {
                     const long long row = c.rows ? (long long)__ldg(c.rows + u.slot0 + i) : u.slot0 + i;
                     if (row >= 0 && row < c.tokens)
-                        src[i] = static_cast<const char*>(c.u) + (row * c.K + 8 * tid) * (F32 ? 4 : 2);
+                        src[i] = c.u + row * c.K + 8 * tid;
                 }
             }
-            float4 ahead[F32 ? SLOTS : 1][2];
-            auto load = [&](int run) {
-                const bool in = run * kRunK + 8 * tid < c.K;
-#pragma unroll
-                for (int i = 0; i < SLOTS; ++i)
-                    if (i < u.slots) {
-                        const float4* q = reinterpret_cast<const float4*>(src[i] + (long long)run * kRunK * 4);
-                        const float4 zero = {0.f, 0.f, 0.f, 0.f};
-                        ahead[F32 ? i : 0][0] = in && src[i] ? __ldg(q) : zero;
-                        ahead[F32 ? i : 0][1] = in && src[i] ? __ldg(q + 1) : zero;
-                    }
-            };
-            if (F32) load(0);
             for (int run = 0; run < runs; ++run) {
                 const bool free = mbar_try_wait(empty0 + 8 * st, phase ^ 1) ||
                                   (!*abort_flag && mbar_wait(empty0 + 8 * st, phase ^ 1, status));
@@ -316,40 +282,14 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                                   there ? w0 + (long long)r * kw + x : c.packed, there);
                     }
                 }
-                if (F32) {
-                    float4 now[SLOTS][2];
+                const bool in = run * kRunK + 8 * tid < c.K;
 #pragma unroll
-                    for (int i = 0; i < SLOTS; ++i) now[i][0] = ahead[F32 ? i : 0][0], now[i][1] = ahead[F32 ? i : 0][1];
-                    if (run + 1 < runs) load(run + 1);
-#pragma unroll
-                    for (int i = 0; i < SLOTS; ++i)
-                        if (i < u.slots) {
-                            const float v[8] = {now[i][0].x, now[i][0].y, now[i][0].z, now[i][0].w,
-                                                now[i][1].x, now[i][1].y, now[i][1].z, now[i][1].w};
-                            uint32_t part[3][4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t a[3], b[3];
-                                split3(v[2 * j], a[0], a[1], a[2]);
-                                split3(v[2 * j + 1], b[0], b[1], b[2]);
-#pragma unroll
-                                for (int q = 0; q < 3; ++q) part[q][j] = __byte_perm(a[q], b[q], 0x7632);
-                            }
-#pragma unroll
-                            for (int q = 0; q < 3; ++q)
-                                sts128(u_st + (3 * i + q) * kUPitch, make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]));
-                        }
-                    mbar_arrive(bar);
-                } else {
-                    const bool in = run * kRunK + 8 * tid < c.K;
-#pragma unroll
-                    for (int i = 0; i < SLOTS; ++i)
-                        if (i < u.slots) {
-                            const bool there = in && src[i];
-                            cp_async16(u_st + i * kUPitch, there ? src[i] + (long long)run * kRunK * 2 : c.u, there);
-                        }
-                }
-                if (!F32 || !TMA) cp_async_arrive(bar);
+                for (int i = 0; i < S::COLS; ++i)
+                    if (i < u.slots) {
+                        const bool there = in && src[i] && LQ_IN_BOUNDS(src[i] - c.u + run * kRunK + 7, (long long)c.tokens * c.K);
+                        cp_async16(u_st + i * kUPitch, there ? src[i] + run * kRunK : c.u, there);
+                    }
+                cp_async_arrive(bar);
                 ++issued;
                 advance();
             }
@@ -371,7 +311,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     int turn = 0;  // the group that takes the next run
     for (long long unit = blockIdx.x; walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
         int tile0;
-        const int h = block_tiles(p, u.blk, tile0), cols = u.slots * p.planes;
+        const int h = block_tiles(p, u.blk, tile0), cols = u.slots;
         float acc[S::H][NT][4];
 #pragma unroll
         for (int i = 0; i < S::H; ++i)
@@ -494,7 +434,7 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-template <int NT, bool TMA, bool F32>
+template <int NT, bool TMA>
 cudaError_t launch_as(const GroupedCall& c, const Plan& p, int h, unsigned* status, cudaStream_t st, int sms) {
     CUtensorMap maps[2] = {};  // sign words of all experts in boxes of 16 h and 16 (h - 1) rows
     if (TMA) {
@@ -515,12 +455,12 @@ cudaError_t launch_as(const GroupedCall& c, const Plan& p, int h, unsigned* stat
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(mma_kernel<NT, TMA, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(mma_kernel<NT, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)(kSmemMax + 1024));
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    mma_kernel<NT, TMA, F32><<<sms, Shape<NT>::THREADS, p.smem, st>>>(maps[0], maps[1], c, p, status);
+    mma_kernel<NT, TMA><<<sms, Shape<NT>::THREADS, p.smem, st>>>(maps[0], maps[1], c, p, status);
     return cudaGetLastError();
 }
 
@@ -529,27 +469,24 @@ cudaError_t launch_nt(const GroupedCall& c, Plan p, int h, unsigned* status, cud
     p.hmax = h;
     p.rp = 16 * h + 4;
     const size_t red = (size_t)Shape<NT>::CONSUMERS * Shape<NT>::COLS * p.rp * 4;
-    const int cols = (c.n < p.per ? c.n : p.per) * p.planes;
+    const int cols = c.n < p.per ? c.n : p.per;
     p.stage_bytes = (h * 2048 + cols * kUPitch + 1023) / 1024 * 1024;
     const int fit = (int)((kSmemMax - kHead - red) / p.stage_bytes);
     p.stages = fit > kMaxStages ? kMaxStages : fit;
     p.smem = 1024 + (size_t)p.stages * p.stage_bytes + kHead + red;
-    const bool tma = c.K % 128 == 0;
-    if (c.u_bf16) return tma ? launch_as<NT, true, false>(c, p, h, status, st, sms) : launch_as<NT, false, false>(c, p, h, status, st, sms);
-    return tma ? launch_as<NT, true, true>(c, p, h, status, st, sms) : launch_as<NT, false, true>(c, p, h, status, st, sms);
+    return c.K % 128 == 0 ? launch_as<NT, true>(c, p, h, status, st, sms) : launch_as<NT, false>(c, p, h, status, st, sms);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
     Plan p{};
-    p.planes = c.u_bf16 ? 1 : 3;
     for (int j = 0; j < 16; ++j) p.shift[j] = 1u << (15 - j);
     // expected columns of an expert that has any: a pass of 8 or of 16
     const int active = c.n < c.experts ? c.n : c.experts;
     const long long each = ((long long)c.n + active - 1) / active;
-    const int nt = each * p.planes > 8 ? 2 : 1;
-    p.per = 8 * nt / p.planes;
+    const int nt = each > 8 ? 2 : 1;
+    p.per = 8 * nt;
     // block height: rounds of blocks over the SMs times their length (a block's fixed cost is about one tile)
     p.tiles = (c.out + 15) / 16;
     const long long passes = (each + p.per - 1) / p.per;

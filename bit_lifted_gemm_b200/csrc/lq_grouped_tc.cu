@@ -396,7 +396,7 @@ cudaError_t launch_as(const GroupedCall& c, unsigned* status, cudaStream_t st, i
     cuuint32_t estride[2] = {1, 1};
     for (int i = 0; i < 2; ++i) {
         cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)(i ? BN : kBox)};
-        if (encode(i ? &map_all : &map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.u), gdim, gstride, box,
+        if (encode(i ? &map_all : &map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(c.u), gdim, gstride, box,
                    estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
@@ -429,7 +429,7 @@ cudaError_t launch_grouped_tc(const GroupedCall& call, void* ws, unsigned* statu
         gather_kernel<<<c.n < 8 * sms ? c.n : 8 * sms, 256, 0, st>>>(c, static_cast<uint4*>(ws));
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        c.u = ws;
+        c.u = static_cast<const uint16_t*>(ws);
         c.tokens = c.n;
         c.rows = nullptr;
     }

@@ -88,6 +88,7 @@ cudaError_t launch_lift_gemv(const void* a, bool a_bf16, int batch, int in, cons
                              float* u, float* o, void* ws, unsigned* status, cudaStream_t st);
 
 struct DecodePlan;
+struct DecodeEpilogue;
 // The quantizers (lq_quant.cu): 32-bit fixed point for the mma.sync kernel
 // (it also clears `nzero` words at `zero`), block-scaled e2m1 digits for the
 // tcgen05 kernel (it also clears the kernel's group counters).
@@ -97,8 +98,14 @@ cudaError_t launch_quant_mx(const float* u, const DecodePlan& p, void* ws, cudaS
 // partial-sum slots in the workspace.
 bool plan_tc(DecodePlan& p);
 size_t tc_slot_bytes(const DecodePlan& p);
-cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodePlan& p, float* o, uint8_t* ws,
-                           unsigned* status, cudaStream_t st);
+cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodePlan& p, float* o,
+                           const DecodeEpilogue* epi, uint8_t* ws, unsigned* status, cudaStream_t st);
+
+// The decode GEMV with the fused epilogue (all fields of `epi` but sums): the
+// same kernels and plan, a workspace of its own size (0: no plan fits).
+size_t gemv_epilogue_workspace_size(int out, int K, int batch);
+cudaError_t launch_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K, const float* u, int batch,
+                                 DecodeEpilogue epi, void* ws, unsigned* status, cudaStream_t st);
 
 // Prefill GEMM on tcgen05. `status` is the device status word.
 cudaError_t launch_gemm(const uint32_t* packed, const float* s, int out, int K,
@@ -111,8 +118,7 @@ struct GroupedCall {
     const uint32_t* packed;  // [experts][out][K/32]
     const float* s;          // [experts][out]
     int experts, out, K;
-    const void* u;  // [tokens][K], fp32 (at most 16 slots, one expert) or bf16
-    bool u_bf16;
+    const uint16_t* u;  // bf16 [tokens][K]
     int tokens;          // rows of u
     const int* rows;     // [n] row of u of each slot, or NULL: slot i takes row i
     const int* offsets;  // [experts + 1] on the device, or NULL
