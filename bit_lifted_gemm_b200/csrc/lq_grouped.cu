@@ -19,7 +19,7 @@ int slots_each(const GroupedCall& c) {
     const int active = c.n < c.experts ? c.n : c.experts;
     return (int)(((long long)c.n + active - 1) / active);
 }
-bool few_rows(const GroupedCall& c) { return slots_each(c) <= 32; }
+bool few_rows(const GroupedCall& c) { return slots_each(c) <= 8; }
 
 }  // namespace
 

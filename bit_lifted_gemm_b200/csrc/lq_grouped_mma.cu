@@ -3,7 +3,7 @@
 //
 //   z[i][r] = s[r] sum_k sigma[r][k] u[row(i)][k] + bias[r]
 //
-// The weights are read once per pass of at most 8 NT columns and bound the kernel,
+// The weights are read once per pass of at most 8 columns and bound the kernel,
 // so the contraction is arranged around them: signs become the A operand of
 // mma.sync m16n8k16 (bf16, fp32 accumulate), 16 weight rows by 16 k, and rows of u
 // are its columns. +-1 and u are exact in bf16, so only the fp32 sums round; NaN and Inf
@@ -49,26 +49,9 @@ constexpr int kMaxStages = 16;
 constexpr size_t kSmemMax = 227 * 1024 - 2048;
 constexpr size_t kHead = 512 + 1024;  // barriers, a block's scales and biases
 
-// H: tiles of 16 rows that a block may have. One n8 tile of columns leaves registers for three
-// groups of consumers, two n8 tiles for two. The block is launched with LAUNCH_REGS a thread, which the
-// consumers raise to CONSUMER_REGS from what the producers and the epilogue's warps give up:
-// (3 x 120 + 2 x 56 of 5 x 96, 2 x 168 + 2 x 88 of 4 x 128).
-template <int NT>
-struct Shape {
-    static constexpr int COLS = 8 * NT, H = NT == 1 ? 8 : 6, GROUPS = NT == 1 ? 3 : 2;
-    static constexpr int CONSUMERS = 4 * GROUPS, PRODUCER = CONSUMERS, EPILOGUE = CONSUMERS + kProducers;
-    static constexpr int THREADS = 32 * (EPILOGUE + 4);
-    static constexpr int LAUNCH_REGS = NT == 1 ? 96 : 128, CONSUMER_REGS = NT == 1 ? 120 : 168, OTHER_REGS = NT == 1 ? 56 : 88;
-    static_assert(CONSUMERS * CONSUMER_REGS + 8 * OTHER_REGS <= (CONSUMERS + 8) * LAUNCH_REGS, "more registers than the block has");
-};
-template <int R>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
+constexpr int COLS = 8, H = 8;  // columns of a pass, tiles of 16 rows that a block may have
+// Two groups of consumers: a third (registers moved over from the other warps) changed no time by more than 2%.
+constexpr int GROUPS = 2, CONSUMERS = 4 * GROUPS, EPILOGUE = CONSUMERS + kProducers, THREADS = 32 * (EPILOGUE + 4);
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -100,15 +83,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
-template <int V>
-struct Int {
-    static constexpr int value = V;
-};
-
 struct Plan {
     uint32_t shift[16];  // 2^(15 - j): kept from the compiler, so that it multiplies (see sign_pair)
     int stages, stage_bytes, rp;    // rp: pitch of a column of the warps' sums, in floats
-    int per;                        // slots of a pass: a column each
     int nblk, tiles, hmax;          // blocks and tiles of an expert's rows; a block has hmax tiles or one less
     size_t smem;
 };
@@ -131,11 +108,10 @@ __device__ __forceinline__ int block_tiles(const Plan& p, int blk, int& tile0) {
 }
 
 // TMA: rows of sign words are 16-byte aligned and come by TMA.
-template <int NT, bool TMA>
-__global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
+template <bool TMA>
+__global__ void __launch_bounds__(THREADS, 1)
     mma_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap wmap_less,
                const __grid_constant__ GroupedCall c, const __grid_constant__ Plan p, unsigned* status) {
-    using S = Shape<NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);  // for the 128-byte swizzle
     const uint32_t ring = smem_addr(smem);
@@ -154,7 +130,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
             mbar_init(full0 + 8 * i, 32 * kProducers + (TMA ? 1 : 0));
             mbar_init(empty0 + 8 * i, 4);
         }
-        mbar_init(red_full, S::CONSUMERS);
+        mbar_init(red_full, CONSUMERS);
         mbar_init(red_empty, 4);
         *abort_flag = 0;
         fence_barrier_init();
@@ -171,15 +147,14 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     auto advance = [&] {
         if (++st == p.stages) st = 0, phase ^= 1;
     };
-    if (warp >= S::EPILOGUE) {
+    if (warp >= EPILOGUE) {
         // ---- epilogue of a block, while the consumers are at the next one: the warps' sums in warp order
-        fewer_registers<S::OTHER_REGS>();
         const int step = c.glu ? 2 : 1, width = c.glu ? c.out / 2 : c.out;
-        for (long long unit = blockIdx.x; walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
+        for (long long unit = blockIdx.x; walk.find<true>(c, COLS, p.nblk, unit, lane, u); unit += gridDim.x) {
             int tile0;
             const int h = block_tiles(p, u.blk, tile0), per_col = 16 * h / step;
             // the rows' scales and biases, one row to a thread, before the sums are there
-            const int tid = threadIdx.x - 32 * S::EPILOGUE;
+            const int tid = threadIdx.x - 32 * EPILOGUE;
             if (tid < 16 * h) {
                 const int row = min(16 * tile0 + tid, c.out - 1);
                 const long long at = (long long)u.e * c.out + row;
@@ -210,13 +185,13 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                         const float* sums = red + slot * p.rp + r;
                         if (c.glu) {
 #pragma unroll
-                            for (int w = 0; w < S::CONSUMERS; ++w) {
-                                const float2 v = *reinterpret_cast<const float2*>(sums + w * S::COLS * p.rp);
+                            for (int w = 0; w < CONSUMERS; ++w) {
+                                const float2 v = *reinterpret_cast<const float2*>(sums + w * COLS * p.rp);
                                 z[0] += v.x, z[1] += v.y;
                             }
                         } else {
 #pragma unroll
-                            for (int w = 0; w < S::CONSUMERS; ++w) z[0] += sums[w * S::COLS * p.rp];
+                            for (int w = 0; w < CONSUMERS; ++w) z[0] += sums[w * COLS * p.rp];
                         }
                         z[0] = scale[r] * z[0] + shift[r];
                         y[m] = activate(z[0], c.act);
@@ -235,18 +210,17 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
         }
         return;
     }
-    if (warp >= S::PRODUCER) {
-        fewer_registers<S::OTHER_REGS>();
+    if (warp >= CONSUMERS) {
         // ---- producers: a thread copies the 16-byte chunk `tid` (8 k) of every column
-        const int tid = threadIdx.x - 32 * S::PRODUCER;
+        const int tid = threadIdx.x - 32 * CONSUMERS;
         bool stop = false;  // the same in all lanes of a warp
         int issued = 0;
-        for (long long unit = blockIdx.x; !stop && walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
+        for (long long unit = blockIdx.x; !stop && walk.find<true>(c, COLS, p.nblk, unit, lane, u); unit += gridDim.x) {
             int tile0;
             const int h = block_tiles(p, u.blk, tile0), rows_left = c.out - 16 * tile0;
-            const uint16_t* src[S::COLS];  // this thread's chunk of run 0 of each slot's row of u, or null
+            const uint16_t* src[COLS];  // this thread's chunk of run 0 of each slot's row of u, or null
 #pragma unroll
-            for (int i = 0; i < S::COLS; ++i) {
+            for (int i = 0; i < COLS; ++i) {
                 src[i] = nullptr;
                 if (i < u.slots) {
                     const long long row = c.rows ? (long long)__ldg(c.rows + u.slot0 + i) : u.slot0 + i;
@@ -265,7 +239,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                 const uint32_t a_st = ring + st * p.stage_bytes, bar = full0 + 8 * st;
                 const uint32_t u_st = a_st + p.hmax * 2048 + tid * 16;
                 if (TMA) {
-                    if (warp == S::PRODUCER && lane == 0) {
+                    if (warp == CONSUMERS && lane == 0) {
                         mbar_arrive_expect_tx(bar, h * 2048);
                         tma_load_2d(a_st, h == p.hmax ? &wmap : &wmap_less, run * kRunWords, u.e * c.out + 16 * tile0, bar);
                     }
@@ -284,7 +258,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                 }
                 const bool in = run * kRunK + 8 * tid < c.K;
 #pragma unroll
-                for (int i = 0; i < S::COLS; ++i)
+                for (int i = 0; i < COLS; ++i)
                     if (i < u.slots) {
                         const bool there = in && src[i] && LQ_IN_BOUNDS(src[i] - c.u + run * kRunK + 7, (long long)c.tokens * c.K);
                         cp_async16(u_st + i * kUPitch, there ? src[i] + run * kRunK : c.u, there);
@@ -295,7 +269,7 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
             }
         }
         cp_async_wait_all();
-        if (TMA && warp == S::PRODUCER)  // no TMA copy is in flight either: the last one of each stage has landed
+        if (TMA && warp == CONSUMERS)  // no TMA copy is in flight either: the last one of each stage has landed
             for (int back = issued < p.stages ? issued : p.stages; back > 0; --back) {
                 const int at = issued - back;
                 mbar_wait(full0 + 8 * (at % p.stages), (at / p.stages) & 1, status);
@@ -304,21 +278,18 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
     }
 
     // ---- consumers
-    more_registers<S::CONSUMER_REGS>();
     int red_phase = 1;
     const int g = lane >> 2, t = lane & 3, quarter = warp & 3, group = warp >> 2;
     const uint32_t rot = t >= 2 ? 0x1032u : 0x3210u;
     int turn = 0;  // the group that takes the next run
-    for (long long unit = blockIdx.x; walk.find<true>(c, p.per, p.nblk, unit, lane, u); unit += gridDim.x) {
+    for (long long unit = blockIdx.x; walk.find<true>(c, COLS, p.nblk, unit, lane, u); unit += gridDim.x) {
         int tile0;
-        const int h = block_tiles(p, u.blk, tile0), cols = u.slots;
-        float acc[S::H][NT][4];
+        const int h = block_tiles(p, u.blk, tile0);
+        float acc[H][4];
 #pragma unroll
-        for (int i = 0; i < S::H; ++i)
+        for (int i = 0; i < H; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.f;
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
         for (int run = 0; run < runs; ++run) {
             if (turn == group) {
                 if (!mbar_try_wait(full0 + 8 * st, phase) && !*abort_flag && !mbar_wait(full0 + 8 * st, phase, status))
@@ -326,78 +297,61 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
                 const uint32_t a_st = ring + st * p.stage_bytes;
                 const uint32_t u_st = a_st + p.hmax * 2048 + quarter * 512 + t * 64 + (t >= 2 ? 32 : 0);
                 const uint32_t u_other = t >= 2 ? -32 : 32;
-                uint32_t b[NT][2][16];
+                uint32_t b[2][16];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int col = 8 * n + g;
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-                            if (col < cols) {
-                                const uint32_t at = u_st + col * kUPitch + x * 256 + half * 16;
-                                lo = lds128(at);
-                                hi = lds128(at + u_other);
-                            }
-                            const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                b[n][x][8 * half + 2 * i] = __byte_perm(l[i], v[i], 0x5410);
-                                b[n][x][8 * half + 2 * i + 1] = __byte_perm(l[i], v[i], 0x7632);
-                            }
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+                        if (g < u.slots) {
+                            const uint32_t at = u_st + g * kUPitch + x * 256 + half * 16;
+                            lo = lds128(at);
+                            hi = lds128(at + u_other);
                         }
-                }
+                        const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            b[x][8 * half + 2 * i] = __byte_perm(l[i], v[i], 0x5410);
+                            b[x][8 * half + 2 * i + 1] = __byte_perm(l[i], v[i], 0x7632);
+                        }
+                    }
                 // row g of tile i: chunk 2 quarter + x, swizzled by the row; rows 8 apart share the swizzle
                 const uint32_t a_row = a_st + g * 128 + t * 4;
-                // K tiles from tile i on, step by step of 128 k; the words of the next step are loaded ahead
+                // Two tiles at a time, so that two chains of accumulation overlap, in steps of 128 k; the words of the
+                // next step are loaded ahead. The second tile may be past the block's (words that are in the
+                // stage, sums that are not used): a path for single tiles made blocks of odd height 3%
+                // faster and the others up to 10% slower.
                 auto load_words = [&](uint32_t (&to)[2][2], int i, int x) {
                     const uint32_t at = a_row + i * 2048 + (((2 * quarter + x) ^ g) << 4);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) to[k][0] = lds32(at + k * 2048), to[k][1] = lds32(at + k * 2048 + 1024);
                 };
-                uint32_t next[2][2];
-                auto tiles = [&](auto many, int i) {
-                    constexpr int K = decltype(many)::value;
+                uint32_t w[2][2], next[2][2];
+                load_words(next, 0, 0);
+#pragma unroll
+                for (int i = 0; i < H; i += 2) {
+                    if (i >= h) break;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        uint32_t w[K][2];
 #pragma unroll
-                        for (int k = 0; k < K; ++k)
+                        for (int k = 0; k < 2; ++k)
                             w[k][0] = __byte_perm(next[k][0], 0, rot), w[k][1] = __byte_perm(next[k][1], 0, rot);
                         if (x == 0)
                             load_words(next, i, 1);
-                        else if (i + 2 < S::H)
+                        else if (i + 2 < H)
                             load_words(next, i + 2, 0);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            uint32_t a[K][4];
+                        for (int j = 0; j < 16; j += 2)
 #pragma unroll
-                            for (int k = 0; k < K; ++k) {
-                                a[k][0] = sign_pair(w[k][0], p, j), a[k][1] = sign_pair(w[k][1], p, j);
-                                a[k][2] = sign_pair(w[k][0], p, j + 1), a[k][3] = sign_pair(w[k][1], p, j + 1);
-                            }
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int k = 0; k < K; ++k)
-                                    mma_bf16(acc[i + k][n], a[k][0], a[k][1], a[k][2], a[k][3], b[n][x][j], b[n][x][j + 1]);
-                        }
+                            for (int k = 0; k < 2; ++k)
+                                mma_bf16(acc[i + k], sign_pair(w[k][0], p, j), sign_pair(w[k][1], p, j),
+                                         sign_pair(w[k][0], p, j + 1), sign_pair(w[k][1], p, j + 1), b[x][j], b[x][j + 1]);
                     }
-                };
-                // two tiles at a time, so that two chains of accumulation overlap. The second may be past the
-                // block's (words that are in the stage, sums that are not used): a path for single tiles made
-                // blocks of odd height 3% faster and the others up to 10% slower.
-                load_words(next, 0, 0);
-#pragma unroll
-                for (int i = 0; i < S::H; i += 2) {
-                    if (i >= h) break;
-                    tiles(Int<2>(), i);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty0 + 8 * st);
             }
-            if (++turn == S::GROUPS) turn = 0;
+            if (++turn == GROUPS) turn = 0;
             advance();
         }
 
@@ -405,13 +359,11 @@ __global__ void __launch_bounds__(Shape<NT>::THREADS, 1)
         if (!mbar_try_wait(red_empty, red_phase) && !*abort_flag && !mbar_wait(red_empty, red_phase, status)) *abort_flag = 1;
         red_phase ^= 1;
 #pragma unroll
-        for (int i = 0; i < S::H; ++i) {
+        for (int i = 0; i < H; ++i) {
             if (i >= h) break;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    red[(warp * S::COLS + 8 * n + 2 * t + (j & 1)) * p.rp + 16 * i + g + (j >> 1) * 8] = acc[i][n][j];
+            for (int j = 0; j < 4; ++j)
+                red[(warp * COLS + 2 * t + (j & 1)) * p.rp + 16 * i + g + (j >> 1) * 8] = acc[i][j];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(red_full);
@@ -434,7 +386,7 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-template <int NT, bool TMA>
+template <bool TMA>
 cudaError_t launch_as(const GroupedCall& c, const Plan& p, int h, unsigned* status, cudaStream_t st, int sms) {
     CUtensorMap maps[2] = {};  // sign words of all experts in boxes of 16 h and 16 (h - 1) rows
     if (TMA) {
@@ -455,26 +407,28 @@ cudaError_t launch_as(const GroupedCall& c, const Plan& p, int h, unsigned* stat
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(mma_kernel<NT, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(mma_kernel<TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)(kSmemMax + 1024));
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    mma_kernel<NT, TMA><<<sms, Shape<NT>::THREADS, p.smem, st>>>(maps[0], maps[1], c, p, status);
+    mma_kernel<TMA><<<sms, THREADS, p.smem, st>>>(maps[0], maps[1], c, p, status);
     return cudaGetLastError();
 }
 
-template <int NT>
-cudaError_t launch_nt(const GroupedCall& c, Plan p, int h, unsigned* status, cudaStream_t st, int sms) {
+// Stages that fit beside blocks of h tiles, in whole rounds of the groups: a stage then belongs to one
+// group, which sees all its phases (a wait goes by a phase's parity; TMA loads may land out of order, so
+// another stage's phase does not tell).
+int ring_stages(const GroupedCall& c, Plan& p, int h) {
     p.hmax = h;
     p.rp = 16 * h + 4;
-    const size_t red = (size_t)Shape<NT>::CONSUMERS * Shape<NT>::COLS * p.rp * 4;
-    const int cols = c.n < p.per ? c.n : p.per;
+    const size_t red = (size_t)CONSUMERS * COLS * p.rp * 4;
+    const int cols = c.n < COLS ? c.n : COLS;
     p.stage_bytes = (h * 2048 + cols * kUPitch + 1023) / 1024 * 1024;
     const int fit = (int)((kSmemMax - kHead - red) / p.stage_bytes);
-    p.stages = fit > kMaxStages ? kMaxStages : fit;
+    p.stages = (fit > kMaxStages ? kMaxStages : fit) / GROUPS * GROUPS;
     p.smem = 1024 + (size_t)p.stages * p.stage_bytes + kHead + red;
-    return c.K % 128 == 0 ? launch_as<NT, true>(c, p, h, status, st, sms) : launch_as<NT, false>(c, p, h, status, st, sms);
+    return p.stages;
 }
 
 }  // namespace
@@ -482,24 +436,21 @@ cudaError_t launch_nt(const GroupedCall& c, Plan p, int h, unsigned* status, cud
 cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
     Plan p{};
     for (int j = 0; j < 16; ++j) p.shift[j] = 1u << (15 - j);
-    // expected columns of an expert that has any: a pass of 8 or of 16
-    const int active = c.n < c.experts ? c.n : c.experts;
-    const long long each = ((long long)c.n + active - 1) / active;
-    const int nt = each > 8 ? 2 : 1;
-    p.per = 8 * nt;
-    // block height: rounds of blocks over the SMs times their length (a block's fixed cost is about one tile)
     p.tiles = (c.out + 15) / 16;
-    const long long passes = (each + p.per - 1) / p.per;
-    long long best_cost = -1;
-    int best = 1;
-    for (int h = 1; h <= (nt == 1 ? Shape<1>::H : Shape<2>::H); ++h) {
-        const long long units = active * passes * ((p.tiles + h - 1) / h);
-        const long long cost = (units + sms - 1) / sms * (h + 1);
-        if (best_cost < 0 || cost < best_cost) best = h, best_cost = cost;
+    const int active = c.n < c.experts ? c.n : c.experts;  // experts expected to have slots, a pass of columns each
+    // Block height: the rounds of blocks over the SMs times their length (a block's fixed cost is about one
+    // tile), blocks as many as fill the rounds; two stages at least for each group of consumers.
+    double best = 0;
+    for (int h = 1; h <= H && ring_stages(c, p, h) >= 2 * GROUPS; ++h) {
+        const long long least = (p.tiles + h - 1) / h, rounds = (active * least + sms - 1) / sms;
+        long long nblk = rounds * sms / active;
+        nblk = nblk < least ? least : nblk > p.tiles ? p.tiles : nblk;
+        const double cost = (double)rounds * ((double)p.tiles / nblk + 1);
+        if (best == 0 || cost < best) best = cost, p.nblk = (int)nblk;
     }
-    p.nblk = (p.tiles + best - 1) / best;
     const int h = (p.tiles + p.nblk - 1) / p.nblk;  // blocks have h or h - 1 tiles
-    return nt == 1 ? launch_nt<1>(c, p, h, status, st, sms) : launch_nt<2>(c, p, h, status, st, sms);
+    ring_stages(c, p, h);
+    return c.K % 128 == 0 ? launch_as<true>(c, p, h, status, st, sms) : launch_as<false>(c, p, h, status, st, sms);
 }
 
 }  // namespace lq

@@ -8,7 +8,7 @@
 // rounded up to 16, so a short tail of an expert costs what it needs. K is walked in
 // steps of 64 (128 for narrow tiles) through a ring of stages. Roles:
 //   warp 0        u rows of the slots by TMA (128-byte swizzle)
-//   warp 1        issues the MMAs (M = 128, K = 16, bf16, fp32 in TMEM)
+//   warp 1        issues the MMAs (M = 128, K = 16, bf16, fp32 in TMEM); narrow tiles: warp 14 too
 //   warps 2..9    two groups that take 128 k in turn; a thread owns one weight row, loads its sign
 //                 words well ahead and stores them as bf16 +-1 into the stage in the swizzled layout
 //   warps 10..13  epilogue of the tile before, from the other of two accumulators: scale, bias,
@@ -34,17 +34,27 @@ using namespace sm100;
 constexpr int BM = 128, BK = 64;        // BK: k of one swizzled tile
 constexpr int A_TILE = BM * BK * 2;
 constexpr int kBox = 64;  // rows of a tiled load of u of a short tile; a long one loads all BN rows at once
-// A stage is SUB tiles of 64 k. tcgen05.commit takes its thread ~450 clocks, and four MMAs of a narrow tile
-// less: narrow tiles commit every 128 k (one thread issuing 64 k steps of N = 64: 500 clocks each).
+constexpr int UNPACK_WARP = 2, EPILOGUE_WARP = 10, ISSUER_WARP = 14;
+
+// A stage is SUB tiles of 64 k. A thread that issues a stage's MMAs spends ~400 clocks more on its commit and
+// on the next wait, which the MMAs of a narrow tile do not cover: narrow tiles commit every 128 k (64 k
+// steps of N = 64 took 500 clocks each, of which the MMAs 190), and the stages of the narrowest alternate
+// between two issuing warps, each with accumulators of its own, added in the epilogue (46 -> 38 us for
+// 64 tokens of 13824 x 12288).
+//
+// A wait goes by a phase's parity, so whoever waits on a stage has to know that the phase before is over. With
+// one issuer stages are freed in order, and a wait on a later stage tells. With two they are not: there every
+// stage belongs to one issuer and one unpack group, by its number's parity (the ring has an even number of
+// stages), which see all its phases.
 template <int BN>
 struct Ring {
+    static constexpr int ISSUERS = BN == 64 ? 2 : 1, THREADS = 32 * (ISSUER_WARP + ISSUERS - 1);
     static constexpr int SUB = BN == 256 ? 1 : 2;
     static constexpr int STAGES = BN == 128 ? 3 : 4;
     static constexpr int A_STAGE = SUB * A_TILE, B_TILE = BN * BK * 2, B_STAGE = SUB * B_TILE;
     static constexpr size_t SMEM_BYTES = 1024 + STAGES * (A_STAGE + B_STAGE) + 256;
+    static_assert(ISSUERS == 1 || (STAGES % 2 == 0 && SUB == 2), "a stage has one issuer and one unpack group");
 };
-constexpr int UNPACK_WARP = 2, EPILOGUE_WARP = 10, THREADS = 32 * 14;
-
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -125,11 +135,12 @@ __device__ __forceinline__ void store_chunk(const GroupedCall& c, float (&z)[32]
 // BN: slots of a full tile. VEC: K a multiple of 128, so that rows of sign words are
 // 16-byte aligned. GATHER: rows are given.
 template <int BN, bool VEC>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
     tc_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_all,
               const __grid_constant__ GroupedCall c, unsigned* status) {
     constexpr int STAGES = Ring<BN>::STAGES, SUB = Ring<BN>::SUB, A_STAGE = Ring<BN>::A_STAGE;
     constexpr int B_STAGE = Ring<BN>::B_STAGE, B_TILE = Ring<BN>::B_TILE, STEP = SUB * BK;
+    constexpr int ISSUERS = Ring<BN>::ISSUERS, ACC = ISSUERS * BN;  // columns of a tile's accumulators
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte aligned for the 128-byte swizzle
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -149,16 +160,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(empty0 + 8 * st, 1);
         }
         for (int a = 0; a < 2; ++a) {
-            mbar_init(acc_full0 + 8 * a, 1);
+            mbar_init(acc_full0 + 8 * a, ISSUERS);
             mbar_init(acc_empty0 + 8 * a, 128);
         }
-        mbar_init(drained, 1);
+        mbar_init(drained, ISSUERS);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmap_u);
     }
     if (warp == 1) {
-        tmem_alloc(smem_addr(tmem_slot), 2 * BN);
+        tmem_alloc(smem_addr(tmem_slot), 2 * ACC);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -228,33 +239,45 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int at = issued - back;
             mbar_wait(full0 + 8 * (at % STAGES), (at / STAGES) & 1, status);
         }
-    } else if (warp == 1) {
-        // ---- MMAs
+    } else if (warp == 1 || warp >= ISSUER_WARP) {
+        // ---- MMAs: of two issuers, each takes every other stage
+        const int issuer = warp == 1 ? 0 : 1;
         int acc = 0, acc_phase = 0;
         const uint64_t a_desc = smem_desc_sw128(sA), b_desc = smem_desc_sw128(sB);
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
             const uint32_t idesc = idesc_bf16_f32(BM, (u.slots + 15) / 16 * 16);
             if (!(go = wait(acc_empty0 + 8 * acc, acc_phase ^ 1))) break;
             tc_fence_after();
+            const uint32_t to = tmem + acc * ACC + issuer * BN;
+            bool first = true;  // the issuer's first stage of the tile
             for (int kb = 0; kb < nkb; ++kb) {
-                if (!(go = ready(full0, 0))) break;
-                poll(full0, 0);
-                tc_fence_after();
-                if (elect_one()) {
-                    // 16 k are 32 bytes of a swizzled row, 2 in the descriptor's address field
-                    const uint64_t a = a_desc + (uint32_t)st * (A_STAGE >> 4), b = b_desc + (uint32_t)st * (B_STAGE >> 4);
+                if (st % ISSUERS == issuer) {
+                    if (ISSUERS == 1) {
+                        if (!(go = ready(full0, 0))) break;
+                        poll(full0, 0);
+                    } else if (!(go = wait(full0 + 8 * st, phase))) {
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        // 16 k are 32 bytes of a swizzled row, 2 in the descriptor's address field
+                        const uint64_t a = a_desc + (uint32_t)st * (A_STAGE >> 4), b = b_desc + (uint32_t)st * (B_STAGE >> 4);
 #pragma unroll
-                    for (int x = 0; x < SUB; ++x)
+                        for (int x = 0; x < SUB; ++x)
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            umma_f16(tmem + acc * BN, a + x * (A_TILE >> 4) + 2 * kk, b + x * (B_TILE >> 4) + 2 * kk, idesc,
-                                     (kb | x | kk) != 0);
-                    umma_commit(empty0 + 8 * st);
-                    if (kb == nkb - 1) umma_commit(acc_full0 + 8 * acc);
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                umma_f16(to, a + x * (A_TILE >> 4) + 2 * kk, b + x * (B_TILE >> 4) + 2 * kk, idesc,
+                                         !first || (x | kk) != 0);
+                        umma_commit(empty0 + 8 * st);
+                    }
+                    __syncwarp();
+                    first = false;
                 }
-                __syncwarp();
                 advance();
             }
+            if (!go) break;
+            if (elect_one()) umma_commit(acc_full0 + 8 * acc);  // arrives at once if no stage of the tile was its own
+            __syncwarp();
             if (++acc == 2) acc = 0, acc_phase ^= 1;
         }
         if (lane == 0) {  // no MMA is in flight when TMEM is freed
@@ -262,7 +285,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_wait(drained, 0, status);
         }
     } else if (warp < EPILOGUE_WARP) {
-        // ---- signs, 128 k at a time (one 16-byte load); of two groups, each takes every other one
+        // ---- signs, 128 k at a time (one 16-byte load); of two groups, each takes every other one (with two
+        // issuers: every other stage)
         constexpr int GROUPS = 2;
         const int group = (warp - UNPACK_WARP) >> 2, row = (threadIdx.x - 32 * UNPACK_WARP) & 127;
         const uint32_t row_off = (row >> 3) * 1024 + (row & 7) * 128, sw = row & 7;
@@ -278,11 +302,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 return make_uint4(__ldg(w0 + min(x, kw - 1)), __ldg(w0 + min(x + 1, kw - 1)), __ldg(w0 + min(x + 2, kw - 1)),
                                   __ldg(w0 + min(x + 3, kw - 1)));
             };
+            const int st0 = st, phase0 = phase;  // ring position of the unit's first k-step
+            const int begin = ISSUERS == 2 ? (group ^ st0) & 1 : group;
             uint4 ahead[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ahead[i] = load(group + GROUPS * i);
-            const int st0 = st, phase0 = phase;  // ring position of the unit's first k-step
-            for (int p0 = group; p0 < pairs && go; p0 += 4 * GROUPS) {
+            for (int i = 0; i < 4; ++i) ahead[i] = load(begin + GROUPS * i);
+            for (int p0 = begin; p0 < pairs && go; p0 += 4 * GROUPS) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int pair = p0 + GROUPS * i;
@@ -319,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         // ---- epilogue: a warp may only reach its own quarter of the TMEM lanes (warp % 4)
         const int q = warp & 3, width = c.glu ? c.out / 2 : c.out;
-        int acc = 0, acc_phase = 0;
+        int acc = 0, acc_phase = 0, issuer0 = 0;  // issuer0: the issuer of the tile's first stage
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
             const int m = u.blk * BM + q * 32 + lane;
             const long long at = (long long)u.e * c.out + min(m, c.out - 1);
@@ -329,11 +354,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
             for (int c0 = 0; c0 < u.slots; c0 += 32) {
                 uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem + acc * BN + ((uint32_t)(q * 32) << 16) + c0, v);
+                const uint32_t from = tmem + acc * ACC + ((uint32_t)(q * 32) << 16) + c0;
+                tmem_ld_32x32b_x32(from + issuer0 * BN, v);
                 tmem_ld_wait();
                 float z[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, __uint_as_float(v[j]), br);
+                for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
+                if (ISSUERS == 2 && nkb > 1) {
+                    tmem_ld_32x32b_x32(from + (issuer0 ^ 1) * BN, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[j] += __uint_as_float(v[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, z[j], br);
                 if (c.o_bf16)
                     store_chunk<true>(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
                 else
@@ -341,6 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             tc_fence_before();
             mbar_arrive(acc_empty0 + 8 * acc);
+            if (ISSUERS == 2) issuer0 ^= nkb & 1;
             if (++acc == 2) acc = 0, acc_phase ^= 1;
         }
     }
@@ -350,7 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 2 * BN);
+        tmem_dealloc(tmem, 2 * ACC);
     }
 }
 
@@ -410,7 +445,7 @@ cudaError_t launch_as(const GroupedCall& c, unsigned* status, cudaStream_t st, i
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    tc_kernel<BN, VEC><<<sms, THREADS, Ring<BN>::SMEM_BYTES, st>>>(map, map_all, c, status);
+    tc_kernel<BN, VEC><<<sms, Ring<BN>::THREADS, Ring<BN>::SMEM_BYTES, st>>>(map, map_all, c, status);
     return cudaGetLastError();
 }
 
