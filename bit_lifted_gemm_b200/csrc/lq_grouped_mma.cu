@@ -47,7 +47,8 @@ constexpr int kProducers = 4;                // warps
 constexpr int kUPitch = kRunK * 2 + 16;      // bytes of one u row of a stage: 16 off a multiple of 32
 constexpr int kMaxStages = 16;
 constexpr size_t kSmemMax = 227 * 1024 - 2048;
-constexpr size_t kHead = 512 + 1024;  // barriers, a block's scales and biases
+static_assert(kProducers % 2 == 0, "stages in rounds of the producers are whole rounds of the two groups");
+constexpr size_t kHead = 512 + 1024 + 512;  // barriers, a block's scales and biases, zeros
 
 constexpr int COLS = 8, H = 8;  // columns of a pass, tiles of 16 rows that a block may have
 // Two groups of consumers: a third (registers moved over from the other warps) changed no time by more than 2%.
@@ -83,6 +84,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
+// One lane of a converged warp, in the form that lets the compiler keep the operands of
+// the instructions behind it in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 struct Plan {
     uint32_t shift[16];  // 2^(15 - j): kept from the compiler, so that it multiplies (see sign_pair)
     int stages, stage_bytes, rp;    // rp: pitch of a column of the warps' sums, in floats
@@ -121,13 +130,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 16 * kMaxStages + 16);
     float* scale = reinterpret_cast<float*>(tail + 512);  // [128], and the biases
     float* shift = scale + 128;
+    const uint32_t zeros = smem_addr(tail + 1536);
     float* red = reinterpret_cast<float*>(tail + kHead);  // [consumers][COLS][rp]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kw = c.K >> 5, runs = (kw + kRunWords - 1) / kRunWords;
 
+    if (threadIdx.x < 128) reinterpret_cast<uint32_t*>(tail + 1536)[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(full0 + 8 * i, 32 * kProducers + (TMA ? 1 : 0));
+            mbar_init(full0 + 8 * i, 32 + (TMA ? 1 : 0));
             mbar_init(empty0 + 8 * i, 4);
         }
         mbar_init(red_full, CONSUMERS);
@@ -211,24 +222,32 @@ __global__ void __launch_bounds__(THREADS, 1)
         return;
     }
     if (warp >= CONSUMERS) {
-        // ---- producers: a thread copies the 16-byte chunk `tid` (8 k) of every column
-        const int tid = threadIdx.x - 32 * CONSUMERS;
+        // ---- producers: each of the four warps fills every fourth run alone, so that four of these chains of
+        // waits and copies run beside one another (one run at a time, a quarter of its copies to a warp, took
+        // 550 to 1300 clocks a run and bounded the kernel)
+        const int mine = warp - CONSUMERS;
         bool stop = false;  // the same in all lanes of a warp
-        int issued = 0;
+        int turn = 0, last = -1, last_phase = 0;
         for (long long unit = blockIdx.x; !stop && walk.find<true>(c, COLS, p.nblk, unit, lane, u); unit += gridDim.x) {
             int tile0;
             const int h = block_tiles(p, u.blk, tile0), rows_left = c.out - 16 * tile0;
-            const uint16_t* src[COLS];  // this thread's chunk of run 0 of each slot's row of u, or null
+            const uint16_t* src[COLS];  // this lane's first 16 bytes of each slot's row of u, or null
 #pragma unroll
             for (int i = 0; i < COLS; ++i) {
                 src[i] = nullptr;
                 if (i < u.slots) {
                     const long long row = c.rows ? (long long)__ldg(c.rows + u.slot0 + i) : u.slot0 + i;
-                    if (row >= 0 && row < c.tokens)
-                        src[i] = c.u + row * c.K + 8 * tid;
+                    if (row >= 0 && row < c.tokens) src[i] = c.u + row * c.K + 8 * lane;
                 }
             }
             for (int run = 0; run < runs; ++run) {
+                const bool own = turn == mine;
+                if (++turn == kProducers) turn = 0;
+                if (!own) {
+                    advance();
+                    continue;
+                }
+                const uint32_t a_st = ring + st * p.stage_bytes, bar = full0 + 8 * st;
                 const bool free = mbar_try_wait(empty0 + 8 * st, phase ^ 1) ||
                                   (!*abort_flag && mbar_wait(empty0 + 8 * st, phase ^ 1, status));
                 if (!__all_sync(0xffffffffu, free)) {
@@ -236,43 +255,49 @@ __global__ void __launch_bounds__(THREADS, 1)
                     stop = true;
                     break;
                 }
-                const uint32_t a_st = ring + st * p.stage_bytes, bar = full0 + 8 * st;
-                const uint32_t u_st = a_st + p.hmax * 2048 + tid * 16;
                 if (TMA) {
-                    if (warp == CONSUMERS && lane == 0) {
+                    if (elect_one()) {
                         mbar_arrive_expect_tx(bar, h * 2048);
                         tma_load_2d(a_st, h == p.hmax ? &wmap : &wmap_less, run * kRunWords, u.e * c.out + 16 * tile0, bar);
                     }
                     __syncwarp();
                 } else {
                     // word x of row r goes to 16-byte chunk (x / 4) ^ (r % 8) of the row, as TMA would put it
-                    const uint32_t* w0 = c.packed + ((long long)u.e * c.out + 16 * tile0) * kw + run * kRunWords;
-                    const int x = tid & 31;
-                    for (int r = tid >> 5; r < 16 * h; r += kProducers) {
-                        const bool there = r < rows_left && run * kRunWords + x < kw &&
-                                           LQ_IN_BOUNDS(((long long)u.e * c.out + 16 * tile0 + r) * kw + run * kRunWords + x,
+                    const uint32_t* w0 = c.packed + ((long long)u.e * c.out + 16 * tile0) * kw + run * kRunWords + lane;
+                    for (int r = 0; r < 16 * h; ++r) {
+                        const bool there = r < rows_left && run * kRunWords + lane < kw &&
+                                           LQ_IN_BOUNDS(((long long)u.e * c.out + 16 * tile0 + r) * kw + run * kRunWords + lane,
                                                         (long long)c.experts * c.out * kw);
-                        cp_async4(a_st + r * 128 + (((x >> 2) ^ (r & 7)) << 4) + (x & 3) * 4,
-                                  there ? w0 + (long long)r * kw + x : c.packed, there);
+                        cp_async4(a_st + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4,
+                                  there ? w0 + (long long)r * kw : c.packed, there);
                     }
                 }
-                const bool in = run * kRunK + 8 * tid < c.K;
+                const uint32_t u_st = a_st + p.hmax * 2048 + lane * 16;
+                const int k_left = c.K - run * kRunK - 8 * lane;  // in 16-byte chunks 256 k apart
 #pragma unroll
                 for (int i = 0; i < COLS; ++i)
                     if (i < u.slots) {
-                        const bool there = in && src[i] && LQ_IN_BOUNDS(src[i] - c.u + run * kRunK + 7, (long long)c.tokens * c.K);
-                        cp_async16(u_st + i * kUPitch, there ? src[i] + run * kRunK : c.u, there);
+                        const uint16_t* from = src[i] + run * kRunK;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const bool there = src[i] && 256 * x < k_left &&
+                                               LQ_IN_BOUNDS(from - c.u + 256 * x + 7, (long long)c.tokens * c.K);
+                            cp_async16(u_st + i * kUPitch + 512 * x, there ? from + 256 * x : c.u, there);
+                        }
                     }
                 cp_async_arrive(bar);
-                ++issued;
+                last = st, last_phase = phase;
                 advance();
             }
         }
         cp_async_wait_all();
-        if (TMA && warp == CONSUMERS)  // no TMA copy is in flight either: the last one of each stage has landed
-            for (int back = issued < p.stages ? issued : p.stages; back > 0; --back) {
-                const int at = issued - back;
-                mbar_wait(full0 + 8 * (at % p.stages), (at / p.stages) & 1, status);
+        // no TMA copy of this warp is in flight either: its stages are filled in turn, so those before its last
+        // one have been waited for by a later wait on their consumers, or are waited for here
+        if (TMA && last >= 0)
+            for (int back = 0; back < p.stages; back += kProducers) {
+                int s = last - back, ph = last_phase;
+                if (s < 0) s += p.stages, ph ^= 1;
+                mbar_wait(full0 + 8 * s, ph, status);
             }
         return;
     }
@@ -295,19 +320,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!mbar_try_wait(full0 + 8 * st, phase) && !*abort_flag && !mbar_wait(full0 + 8 * st, phase, status))
                     *abort_flag = 1;
                 const uint32_t a_st = ring + st * p.stage_bytes;
-                const uint32_t u_st = a_st + p.hmax * 2048 + quarter * 512 + t * 64 + (t >= 2 ? 32 : 0);
                 const uint32_t u_other = t >= 2 ? -32 : 32;
+                // columns past the pass's read zeros (no branch around the loads: it cost 500 clocks a run)
+                const uint32_t u_at = (g < u.slots ? a_st + p.hmax * 2048 + g * kUPitch + quarter * 512 + t * 64 : zeros) + (t >= 2 ? 32 : 0);
                 uint32_t b[2][16];
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        uint4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-                        if (g < u.slots) {
-                            const uint32_t at = u_st + g * kUPitch + x * 256 + half * 16;
-                            lo = lds128(at);
-                            hi = lds128(at + u_other);
-                        }
+                        const uint32_t at = u_at + x * 256 + half * 16;
+                        const uint4 lo = lds128(at), hi = lds128(at + u_other);
                         const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -416,9 +438,9 @@ cudaError_t launch_as(const GroupedCall& c, const Plan& p, int h, unsigned* stat
     return cudaGetLastError();
 }
 
-// Stages that fit beside blocks of h tiles, in whole rounds of the groups: a stage then belongs to one
-// group, which sees all its phases (a wait goes by a phase's parity; TMA loads may land out of order, so
-// another stage's phase does not tell).
+// Stages that fit beside blocks of h tiles, in whole rounds of the producers and of the groups: a stage then
+// belongs to one of each, which see all its phases (a wait goes by a phase's parity; stages are filled
+// and freed out of order, so another stage's phase does not tell).
 int ring_stages(const GroupedCall& c, Plan& p, int h) {
     p.hmax = h;
     p.rp = 16 * h + 4;
@@ -426,7 +448,7 @@ int ring_stages(const GroupedCall& c, Plan& p, int h) {
     const int cols = c.n < COLS ? c.n : COLS;
     p.stage_bytes = (h * 2048 + cols * kUPitch + 1023) / 1024 * 1024;
     const int fit = (int)((kSmemMax - kHead - red) / p.stage_bytes);
-    p.stages = (fit > kMaxStages ? kMaxStages : fit) / GROUPS * GROUPS;
+    p.stages = (fit > kMaxStages ? kMaxStages : fit) / kProducers * kProducers;
     p.smem = 1024 + (size_t)p.stages * p.stage_bytes + kHead + red;
     return p.stages;
 }
@@ -439,9 +461,9 @@ cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStrea
     p.tiles = (c.out + 15) / 16;
     const int active = c.n < c.experts ? c.n : c.experts;  // experts expected to have slots, a pass of columns each
     // Block height: the rounds of blocks over the SMs times their length (a block's fixed cost is about one
-    // tile), blocks as many as fill the rounds; two stages at least for each group of consumers.
+    // tile), blocks as many as fill the rounds.
     double best = 0;
-    for (int h = 1; h <= H && ring_stages(c, p, h) >= 2 * GROUPS; ++h) {
+    for (int h = 1; h <= H && ring_stages(c, p, h) > 0; ++h) {
         const long long least = (p.tiles + h - 1) / h, rounds = (active * least + sms - 1) / sms;
         long long nblk = rounds * sms / active;
         nblk = nblk < least ? least : nblk > p.tiles ? p.tiles : nblk;
