@@ -78,19 +78,38 @@ __device__ __forceinline__ void store_elem(void* p, long long i, bool bf16, floa
         static_cast<float*>(p)[i] = v;
 }
 
-// The decode kernels' epilogue of one element: z of weight row r (scale applied, no bias yet) of column
-// c. Called by the lanes of rows 2i and 2i + 1 together, which are neighbours, when gated.
-__device__ __forceinline__ void finish_elem(const DecodeEpilogue& e, int out, int c, int r, float z, int lane) {
-    if (e.bias) z += __ldg(e.bias + r);
+// The decode kernels' epilogue of weight row r of `count` columns from column 0 on, z with the scale applied and
+// no bias yet. Called by the lanes of rows 2i and 2i + 1 together, which are neighbours, when gated. The
+// choices are made outside the loops over the columns.
+template <int N>
+__device__ __forceinline__ void finish_row(const DecodeEpilogue& e, int out, int c0, int count, int r, float (&z)[N], int lane) {
+    const float bias = e.bias ? __ldg(e.bias + r) : 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) z[c] += bias;
+    long long at = (long long)c0 * out + r, step = out;  // of column c0, and from one to the next
     if (e.glu) {
-        const float other = __shfl_xor_sync(3u << (lane & 30), z, 1);
+        float other[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) other[c] = __shfl_xor_sync(3u << (lane & 30), z[c], 1);
         if (r & 1) return;
-        z = activate(z, e.act) * other;
+        activate_all(z, e.act);
+#pragma unroll
+        for (int c = 0; c < N; ++c) z[c] *= other[c];
+        step = out / 2;
+        at = c0 * step + r / 2;
     } else {
-        z = activate(z, e.act);
+        activate_all(z, e.act);
     }
-    const long long at = e.glu ? (long long)c * (out / 2) + r / 2 : (long long)c * out + r;
-    store_elem(e.o, at, e.o_bf16, e.residual ? z + load_elem(e.residual, at, e.o_bf16) : z);
+    if (e.residual) {
+        float res[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) res[c] = c < count ? load_elem(e.residual, at + c * step, e.o_bf16) : 0.f;
+#pragma unroll
+        for (int c = 0; c < N; ++c) z[c] += res[c];
+    }
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+        if (c < count) store_elem(e.o, at + c * step, e.o_bf16, z[c]);
 }
 
 }  // namespace lq

@@ -650,10 +650,12 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
         if constexpr (EPI) {
             float* part = p.epi.sums + (long long)(p.c0 + c) * p.out + m;
             if (p.accumulate) res += *part;
-            if (p.last)
-                finish_elem(p.epi, p.out, p.c0 + c, m, res, lane);
-            else
+            if (p.last) {
+                float z[1] = {res};
+                finish_row(p.epi, p.out, p.c0 + c, 1, m, z, lane);
+            } else {
                 *part = res;
+            }
             continue;
         }
         float* outp = p.o + (long long)(p.c0 + c) * p.out + m;
@@ -941,6 +943,43 @@ cudaError_t launch_gemv_epilogue(const uint32_t* packed, const float* s, int out
     const DecodePlan pl = make_decode_plan(out, K, batch);
     epi.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.bytes);
     return launch_decode(pl, packed, s, u, nullptr, &epi, ws, status, st);
+}
+
+namespace {
+
+// bf16 u as fp32, eight elements a thread.
+__global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ u, int count, float4* __restrict__ to) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the GEMV's weights may be requested meanwhile
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= count) return;
+    const uint4 v = __ldg(u + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[2 * j] = __uint_as_float(w[j] << 16), f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    to[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
+    to[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+size_t widened_bytes(int K, int batch) { return align256((size_t)batch * K * 4); }
+
+}  // namespace
+
+size_t gemv_epilogue_bf16_workspace_size(int out, int K, int batch) {
+    const size_t rest = gemv_epilogue_workspace_size(out, K, batch);
+    return rest ? widened_bytes(K, batch) + rest : 0;
+}
+
+cudaError_t launch_gemv_epilogue_bf16(const uint32_t* packed, const float* s, int out, int K, const uint16_t* u, int batch,
+                                      const DecodeEpilogue& epi, void* ws, unsigned* status, cudaStream_t st) {
+    const long long count = (long long)batch * K / 8;
+    float* wide = static_cast<float*>(ws);
+    widen_kernel<<<(int)((count + 255) / 256), 256, 0, st>>>(reinterpret_cast<const uint4*>(u), (int)count,
+                                                            reinterpret_cast<float4*>(wide));
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_gemv_epilogue(packed, s, out, K, wide, batch, epi, static_cast<uint8_t*>(ws) + widened_bytes(K, batch), status,
+                                st);
 }
 
 cudaError_t launch_lift_gemv(const void* a, bool a_bf16, int batch, int in, const float* tinv, int tblk,

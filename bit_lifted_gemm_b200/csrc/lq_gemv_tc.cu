@@ -569,8 +569,10 @@ __global__ void __launch_bounds__(tc_threads(MT), 1)
                 const long long r = g * kRG + t * 128 + 32 * q + lane;
                 if (r >= p.out) return;
                 const double sr = (double)__ldg(p.s + r);
+                float z[EPI ? kCmax : 1];
 #pragma unroll
                 for (int c = 0; c < kCmax; ++c) {
+                    if constexpr (EPI) z[c] = 0.f;
                     if (c >= p.batch) continue;
                     const int mode = col[4 * c + 1];
                     float res;
@@ -588,10 +590,11 @@ __global__ void __launch_bounds__(tc_threads(MT), 1)
                         res = __int_as_float(0x7fc00000);
                     }
                     if constexpr (EPI)
-                        finish_elem(p.epi, p.out, c, (int)r, res, lane);
+                        z[c] = res;
                     else
                         p.o[(size_t)c * p.out + r] = res;
                 }
+                if constexpr (EPI) finish_row(p.epi, p.out, 0, p.batch, (int)r, z, lane);
             };
             // ---- drain tile by tile: sum the planes of each column (plane p =
             // columns p * bpad ..), then store the result (the group is this

@@ -9,7 +9,7 @@
 // steps of 64 (128 for narrow tiles) through a ring of stages. Roles:
 //   warp 0        u rows of the slots by TMA (128-byte swizzle)
 //   warp 1        issues the MMAs (M = 128, K = 16, bf16, fp32 in TMEM); narrow tiles: warp 14 too
-//   warps 2..9    two groups that take 128 k in turn; a thread owns one weight row, loads its sign
+//   warps 2..9    two groups that fill the stages in turn; a thread owns one weight row, loads its sign
 //                 words well ahead and stores them as bf16 +-1 into the stage in the swizzled layout
 //   warps 10..13  epilogue of the tile before, from the other of two accumulators: scale, bias,
 //                 activation or gate, residual, one rounding, store. A thread owns one weight
@@ -37,23 +37,23 @@ constexpr int kBox = 64;  // rows of a tiled load of u of a short tile; a long o
 constexpr int UNPACK_WARP = 2, EPILOGUE_WARP = 10, ISSUER_WARP = 14;
 
 // A stage is SUB tiles of 64 k. A thread that issues a stage's MMAs spends ~400 clocks more on its commit and
-// on the next wait, which the MMAs of a narrow tile do not cover: narrow tiles commit every 128 k (64 k
-// steps of N = 64 took 500 clocks each, of which the MMAs 190), and the stages of the narrowest alternate
-// between two issuing warps, each with accumulators of its own, added in the epilogue (46 -> 38 us for
-// 64 tokens of 13824 x 12288).
+// on the next wait, which the MMAs of a narrow tile do not cover: there the stages alternate between two
+// issuing warps, each with accumulators of its own, added in the epilogue (64 tokens of 13824 x 12288:
+// 46 -> 38 us), and the narrowest tiles commit every 128 k (64 k steps of N = 64 took one issuer 500
+// clocks each, of which the MMAs 190).
 //
-// A wait goes by a phase's parity, so whoever waits on a stage has to know that the phase before is over. With
-// one issuer stages are freed in order, and a wait on a later stage tells. With two they are not: there every
-// stage belongs to one issuer and one unpack group, by its number's parity (the ring has an even number of
-// stages), which see all its phases.
+// A wait goes by a phase's parity, so whoever waits on a stage has to know that the phase before is over, and
+// stages are freed and filled out of order. So every stage belongs to one unpack group and one issuer, by its
+// number's parity (rings have an even number of stages), which see all its phases; the loads of u and a single
+// issuer see all phases of all stages.
 template <int BN>
 struct Ring {
-    static constexpr int ISSUERS = BN == 64 ? 2 : 1, THREADS = 32 * (ISSUER_WARP + ISSUERS - 1);
-    static constexpr int SUB = BN == 256 ? 1 : 2;
-    static constexpr int STAGES = BN == 128 ? 3 : 4;
+    static constexpr int ISSUERS = BN == 256 ? 1 : 2, THREADS = 32 * (ISSUER_WARP + ISSUERS - 1);
+    static constexpr int SUB = BN == 64 ? 2 : 1;
+    static constexpr int STAGES = BN == 128 ? 6 : 4;
+    static_assert(STAGES % 2 == 0, "a stage has one unpack group and one issuer");
     static constexpr int A_STAGE = SUB * A_TILE, B_TILE = BN * BK * 2, B_STAGE = SUB * B_TILE;
     static constexpr size_t SMEM_BYTES = 1024 + STAGES * (A_STAGE + B_STAGE) + 256;
-    static_assert(ISSUERS == 1 || (STAGES % 2 == 0 && SUB == 2), "a stage has one issuer and one unpack group");
 };
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -285,56 +285,60 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
             mbar_wait(drained, 0, status);
         }
     } else if (warp < EPILOGUE_WARP) {
-        // ---- signs, 128 k at a time (one 16-byte load); of two groups, each takes every other one (with two
-        // issuers: every other stage)
-        constexpr int GROUPS = 2;
+        // ---- signs: each of two groups fills every other stage
+        constexpr int WORDS = 2 * SUB, AHEAD = 16 / WORDS;  // sign words of a row and stage; stages loaded ahead
         const int group = (warp - UNPACK_WARP) >> 2, row = (threadIdx.x - 32 * UNPACK_WARP) & 127;
         const uint32_t row_off = (row >> 3) * 1024 + (row & 7) * 128, sw = row & 7;
-        const int pairs = (c.K + 127) / 128;
         for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
             const int r = min(u.blk * BM + row, c.out - 1);  // rows past `out` are computed but not stored
-            // The words of 128 k. Past the row's end its last words are read again: u is
-            // zero there. (No branch: a load merged with another value would be waited for at once.)
+            // Past the row's end its last words are read again: u is zero there. (No branch: a load merged with
+            // another value would be waited for at once.)
             const uint32_t* w0 = c.packed + ((long long)u.e * c.out + r) * kw;
-            auto load = [&](int pair) {
-                const int x = 4 * pair;
-                if constexpr (VEC) return __ldg(reinterpret_cast<const uint4*>(w0 + min(x, kw - 4)));
-                return make_uint4(__ldg(w0 + min(x, kw - 1)), __ldg(w0 + min(x + 1, kw - 1)), __ldg(w0 + min(x + 2, kw - 1)),
-                                  __ldg(w0 + min(x + 3, kw - 1)));
+            auto load = [&](int kb, uint32_t (&to)[WORDS]) {
+                const int x = WORDS * kb;
+                if constexpr (VEC && SUB == 2) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(w0 + min(x, kw - 4)));
+                    to[0] = v.x, to[1] = v.y, to[2] = v.z, to[WORDS - 1] = v.w;
+                } else if constexpr (VEC) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(w0 + min(x, kw - 2)));
+                    to[0] = v.x, to[1] = v.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < WORDS; ++i) to[i] = __ldg(w0 + min(x + i, kw - 1));
+                }
             };
-            const int st0 = st, phase0 = phase;  // ring position of the unit's first k-step
-            const int begin = ISSUERS == 2 ? (group ^ st0) & 1 : group;
-            uint4 ahead[4];
+            const int st0 = st, phase0 = phase;  // ring position of the unit's first stage
+            const int begin = (group ^ st0) & 1;
+            uint32_t ahead[AHEAD][WORDS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ahead[i] = load(begin + GROUPS * i);
-            for (int p0 = begin; p0 < pairs && go; p0 += 4 * GROUPS) {
+            for (int i = 0; i < AHEAD; ++i) load(begin + 2 * i, ahead[i]);
+            for (int kb0 = begin; kb0 < nkb && go; kb0 += 2 * AHEAD) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pair = p0 + GROUPS * i;
-                    if (pair >= pairs || !go) break;
-                    const uint32_t w[4] = {ahead[i].x, ahead[i].y, ahead[i].z, ahead[i].w};
-                    ahead[i] = load(pair + 4 * GROUPS);
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int kb = kb0 + 2 * i;
+                    if (kb >= nkb || !go) break;
+                    uint32_t w[WORDS];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int kb = SUB == 2 ? pair : 2 * pair + half;
-                        if (kb >= nkb || !go) break;
-                        const int at = st0 + kb, s = at % STAGES, ph = phase0 ^ ((at / STAGES) & 1);
+                    for (int x = 0; x < WORDS; ++x) w[x] = ahead[i][x];
+                    load(kb + 2 * AHEAD, ahead[i]);
+                    const int at = st0 + kb, s = at % STAGES, ph = phase0 ^ ((at / STAGES) & 1);
+#pragma unroll
+                    for (int half = 0; half < SUB; ++half) {
                         uint32_t v[32];
                         expand16(w[2 * half], v);
                         expand16(w[2 * half] >> 16, v + 8);
                         expand16(w[2 * half + 1], v + 16);
                         expand16(w[2 * half + 1] >> 16, v + 24);
-                        if (SUB == 1 || half == 0)
+                        if (half == 0)
                             if (!(go = wait(empty0 + 8 * s, ph ^ 1))) break;
-                        const uint32_t dst = sA + s * A_STAGE + (SUB == 2 ? half * A_TILE : 0) + row_off;
+                        const uint32_t dst = sA + s * A_STAGE + half * A_TILE + row_off;
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             st_shared_v4(dst + ((q ^ sw) << 4), v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                        if (SUB == 1 || half == 1) {
-                            fence_proxy_async_smem();
-                            mbar_arrive(full0 + 8 * s);
-                        }
                     }
+                    if (!go) break;
+                    fence_proxy_async_smem();
+                    mbar_arrive(full0 + 8 * s);
                 }
             }
             st = st0 + nkb;

@@ -106,6 +106,10 @@ cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodeP
 size_t gemv_epilogue_workspace_size(int out, int K, int batch);
 cudaError_t launch_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K, const float* u, int batch,
                                  DecodeEpilogue epi, void* ws, unsigned* status, cudaStream_t st);
+// The same for bf16 u, made fp32 in the workspace first.
+size_t gemv_epilogue_bf16_workspace_size(int out, int K, int batch);
+cudaError_t launch_gemv_epilogue_bf16(const uint32_t* packed, const float* s, int out, int K, const uint16_t* u, int batch,
+                                      const DecodeEpilogue& epi, void* ws, unsigned* status, cudaStream_t st);
 
 // Prefill GEMM on tcgen05. `status` is the device status word.
 cudaError_t launch_gemm(const uint32_t* packed, const float* s, int out, int K,

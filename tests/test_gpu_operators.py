@@ -85,6 +85,40 @@ def test_layer_epilogue(lq, out, K, tokens, which):
     plain.assert_close(f64(got), want, tol, o_t == "bf16")
 
 
+@pytest.mark.parametrize("K", [32, 96, 160, 288, 384, 1056])
+@pytest.mark.parametrize("tokens", [3, 8, 9, 64, 65, 128, 129, 260])
+def test_many_tiles_of_few_steps(lq, K, tokens):
+    """More tiles than the persistent kernels have CTAs, with one, odd and even numbers of k-steps each: the rings and
+    their owners carry on from tile to tile."""
+    out = 40000
+    rng = np.random.default_rng([20, K, tokens])
+    packed, s = make_layer(rng, (), out, K)
+    u = bf16(rng.standard_normal((tokens, K)))
+    rows = np.sort(rng.choice(out, 3000, replace=False))
+    rows[-1], rows[0] = out - 1, 0
+    want, tol = plain.layer(packed[rows], s[rows].astype(np.float64), u)
+    args = dev(packed), gpu(s), gpu(u, True)
+    first = lq.gemm_epilogue(*args)
+    plain.assert_close(f64(first)[:, rows], want, tol, False)
+    for _ in range(5):
+        assert bool((lq.gemm_epilogue(*args) == first).all())
+
+
+@pytest.mark.parametrize("each", [1, 5, 8, 20, 70, 150])
+@pytest.mark.parametrize("K", [96, 288, 1120])
+def test_many_experts_of_few_steps(lq, each, K):
+    """The same over experts of uneven sizes, some empty."""
+    rng = np.random.default_rng([21, each, K])
+    E, out = 40, 1100
+    sizes = rng.integers(0, 2 * each + 1, E)
+    sizes[3], sizes[7] = 0, 2 * each
+    case = grouped_case(rng, E, out, K, sizes, True)
+    packed, s, offsets, n, rows, u = case
+    got = call_grouped(lq, *case, o_dtype="f32")
+    want, tol, _ = plain.grouped(packed, s.astype(np.float64), u, offsets, n, rows)
+    plain.assert_close(f64(got), want, tol, False)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("glu", [False, True])
 def test_activations_over_their_range(lq, act, glu):
