@@ -21,9 +21,13 @@ int slots_each(const GroupedCall& c) {
     return (int)(((long long)c.n + active - 1) / active);
 }
 
-// One or two tokens through one layer: the decode GEMV on u made fp32, unless its plan does not fit.
+// Tokens of one layer that take the decode GEMV on u made fp32 (1.5 us), unless its plan does not fit: one or two,
+// and nine to sixteen where the tcgen05 kernel's 128-row tiles exceed the 148 SMs. Measured in us, this path
+// against the kernel that would take them else: 13824 x 12288 at 1 / 2 / 16 tokens 12.4 / 14.4 / 42 against
+// 17.7 / 18.9 / 37, 28672 x 20480 26.4 / 36.4 / 83 against 58 / 59 / 130, 4096 x 10240 8.7 / 10.5 / 34 against 10.6 / 10.8 / 31.
 size_t decode_workspace(const GroupedCall& c) {
-    return c.experts == 1 && !c.offsets && c.n <= 2 ? gemv_epilogue_bf16_workspace_size(c.out, c.K, c.n) : 0;
+    if (c.experts != 1 || c.offsets || c.n > 16 || (c.n > 2 && (c.n <= 8 || c.out <= 148 * 128))) return 0;
+    return gemv_epilogue_bf16_workspace_size(c.out, c.K, c.n);
 }
 
 // Up to eight slots an expert, one pass of the mma.sync kernel, which reads the weights once for all of them.

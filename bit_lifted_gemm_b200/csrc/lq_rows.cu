@@ -13,23 +13,29 @@ namespace cg = cooperative_groups;
 
 // ---- lq_group_rows: a stable counting sort of the ids, in one launch
 //
-// One cluster (of one CTA for few ids, else eight) cuts the ids into one contiguous run per
+// One cluster (of 1, 8 or 16 CTAs) cuts the ids into one contiguous run per
 // warp. Each warp counts its run's ids per expert in shared memory of its own (32 ids at a time:
-// lanes with equal ids find one another, their lowest lane adds). Prefix sums over the warps,
+// lanes with equal ids find one another by ballots, their lowest lane adds). Prefix sums over the warps,
 // over the cluster's CTAs (distributed shared memory) and over the experts give every warp the
 // first slot of its ids of each expert; walking its run again, it hands them out in order. So
 // slots do not depend on timing and no global scratch is needed. Latency bounds it: loads of
 // eight rounds are issued together, and each round is a chain through shared memory.
-constexpr int kMaxWarps = 32, kRounds = 8, kCluster = 8;
+constexpr int kMaxWarps = 32, kRounds = 8, kCluster = 16;
 
-// Lanes of the warp with this id, and this lane's place among them.
-__device__ __forceinline__ int rank_among_equals(int id, int lane, unsigned& peers) {
-    peers = __match_any_sync(0xffffffffu, id);
+// Lanes of the warp with this id (below 2^bits), and this lane's place among them: one ballot a bit. (A match
+// instruction takes the SM ~64 clocks, which bounded the kernel: 35 us for 131072 ids of 128 experts.)
+__device__ __forceinline__ int rank_among_equals(unsigned id, int bits, int lane, unsigned& peers) {
+    peers = 0xffffffffu;
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (id >> b) & 1u;
+        const unsigned v = __ballot_sync(0xffffffffu, set);
+        peers &= set ? v : ~v;
+    }
     return __popc(peers & ((1u << lane) - 1u));
 }
 
 __global__ void __launch_bounds__(32 * kMaxWarps)
-    group_kernel(const int* __restrict__ ids, int n, int topk, int experts, int* __restrict__ offsets,
+    group_kernel(const int* __restrict__ ids, int n, int topk, int experts, int bits, int* __restrict__ offsets,
                  int* __restrict__ rows, int* __restrict__ slots) {
     extern __shared__ int smem[];
     cg::cluster_group cluster = cg::this_cluster();
@@ -46,18 +52,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) count[i] = 0;
     __syncthreads();
     for (long long i0 = lo; i0 < hi; i0 += 32 * kRounds) {
-        int id[kRounds];
+        unsigned id[kRounds];  // experts: left out
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             const long long i = i0 + 32 * r + lane;
-            id[r] = i < hi && LQ_IN_BOUNDS(i, n) ? __ldg(ids + i) : -1;
+            id[r] = i < hi && LQ_IN_BOUNDS(i, n) ? min((unsigned)__ldg(ids + i), (unsigned)experts) : experts;
         }
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             if (i0 + 32 * r >= hi) break;
             unsigned peers;
-            const int rank = rank_among_equals(id[r], lane, peers);
-            if (rank == 0 && id[r] >= 0 && id[r] < experts) mine[id[r]] += __popc(peers);
+            const int rank = rank_among_equals(id[r], bits, lane, peers);
+            if (rank == 0 && id[r] < (unsigned)experts) mine[id[r]] += __popc(peers);
             __syncwarp();
         }
     }
@@ -106,19 +112,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     if (cta == 0 && threadIdx.x == 0) offsets[experts] = kept;
     __syncthreads();
     for (long long i0 = lo; i0 < hi; i0 += 32 * kRounds) {
-        int id[kRounds];
+        unsigned id[kRounds];  // experts: left out
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             const long long i = i0 + 32 * r + lane;
-            id[r] = i < hi && LQ_IN_BOUNDS(i, n) ? __ldg(ids + i) : -1;
+            id[r] = i < hi && LQ_IN_BOUNDS(i, n) ? min((unsigned)__ldg(ids + i), (unsigned)experts) : experts;
         }
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
             const long long i = i0 + 32 * r + lane;
             if (i0 + 32 * r >= hi) break;
             unsigned peers;
-            const int rank = rank_among_equals(id[r], lane, peers);
-            const bool there = id[r] >= 0 && id[r] < experts;
+            const int rank = rank_among_equals(id[r], bits, lane, peers);
+            const bool there = id[r] < (unsigned)experts;
             const int first = there ? mine[id[r]] : 0;
             __syncwarp();
             if (there && rank == 0) mine[id[r]] = first + __popc(peers);
@@ -217,20 +223,24 @@ cudaError_t launch_combine(const void* y, int n, int width, const int* slots, co
 cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts, int* offsets, int* rows, int* slots,
                               cudaStream_t st) {
     const int n = tokens * topk;
-    // one CTA up to 2048 ids (a cluster's start and two barriers cost more than they save); as many warps as
-    // have 64 ids each, and as their counts fit in shared memory
-    const int ctas = n <= 2048 ? 1 : kCluster;
+    // One CTA up to 512 ids (a cluster's start and two barriers cost more than they save: 32 ids 3.7 us, 2048 ids
+    // 8.4 us against 6 for eight CTAs), sixteen from 16384 on (131072 ids: 17.5 us against 28); as many warps
+    // as have 64 ids each, and as their counts fit in shared memory
+    const int ctas = n <= 512 ? 1 : n <= 16384 ? 8 : kCluster;
     const int room = 160 * 1024 / (4 * experts);
     int warps = (n + 64 * ctas - 1) / (64 * ctas);
     warps = warps > kMaxWarps ? kMaxWarps : warps;
     warps = warps > room ? room : warps;
     warps = warps < 4 ? 4 : warps;
+    int bits = 0;  // of ids 0..experts, the last for those left out
+    while (experts >> bits) ++bits;
     const size_t smem = ((size_t)(warps + 2) * experts + 32) * 4;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
         cudaError_t e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
@@ -245,7 +255,7 @@ cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts,
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, group_kernel, ids, n, topk, experts, offsets, rows, slots);
+    return cudaLaunchKernelEx(&cfg, group_kernel, ids, n, topk, experts, bits, offsets, rows, slots);
 }
 
 cudaError_t launch_combine_rows(const void* y, bool bf16, int n, int width, const int* slots, const float* weights,
