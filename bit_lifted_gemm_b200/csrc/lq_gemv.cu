@@ -181,7 +181,27 @@ struct GemvArgs {
     int accumulate;   // 1: o += this launch's result
     int last;         // 1: no launch over K follows for these columns
     DecodeEpilogue epi;
+    // slots of experts (EPI): slot i, row i of u and of o, is contracted by CTAs [i * per, (i + 1) * per) with the layer of the
+    // expert whose range holds it; packed, s and bias hold all experts' rows
+    int per;             // 0: one layer
+    const int* offsets;  // [experts + 1]
+    int experts, nslots;
 };
+
+// The expert e with offsets[e] <= slot < offsets[e + 1] (cut to 0..nslots), or -1. Warp-collective.
+__device__ __forceinline__ int expert_of(const int* offsets, int experts, int nslots, int slot, int lane) {
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+        const int e = e0 + lane;
+        bool holds = false;
+        if (e < experts) {
+            const int lo = min(max(__ldg(offsets + e), 0), nslots);
+            holds = lo <= slot && slot < min(__ldg(offsets + e + 1), nslots);
+        }
+        const unsigned found = __ballot_sync(0xffffffffu, holds);
+        if (found) return e0 + __ffs(found) - 1;
+    }
+    return -1;
+}
 
 // Shared-memory carve-up (offsets from a 1024-byte-aligned base).
 struct Layout {
@@ -221,8 +241,18 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
     uint8_t* smem = smem_raw + ((1024u - (sm100::smem_addr(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int gbeg = split_point(blockIdx.x, p.ngroups, gridDim.x);
-    const int gend = split_point(blockIdx.x + 1, p.ngroups, gridDim.x);
+    int cta = blockIdx.x, ctas = gridDim.x, c0 = p.c0;  // this CTA's place, and the first column
+    long long wrow = 0;                                 // first weight row of the layer
+    if (EPI && p.per) {
+        const int slot = cta / p.per, e = expert_of(p.offsets, p.experts, p.nslots, slot, lane);
+        if (e < 0) return;  // a slot of no expert: the whole CTA
+        cta -= slot * p.per;
+        ctas = p.per;
+        c0 = slot;
+        wrow = (long long)e * p.out;
+    }
+    const int gbeg = split_point(cta, p.ngroups, ctas);
+    const int gend = split_point(cta + 1, p.ngroups, ctas);
     const int m0 = 16 * gbeg;
     const int spg = p.kwc / kStepWords;              // steps per group
     const int tpg = (spg + TS - 1) / TS;             // tiles per group
@@ -249,7 +279,7 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
     if (TMA) {
         const int gl = t0 / tpg;
         nxt_xs = (t0 - gl * tpg) * TS;
-        nxt_y = m0 + 16 * gl;
+        nxt_y = (int)wrow + m0 + 16 * gl;
     }
     auto issue = [&]() {
         const int slot = (nxt - t0) & (STAGES - 1);
@@ -293,7 +323,7 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
     // s of this CTA's rows is a weight: requested now, stored to shared memory
     // after the dependency wait (its latency hides behind the wait)
     const int nrow = (gend - gbeg) * 16;
-    const float s_own = threadIdx.x < nrow && m0 + threadIdx.x < p.out ? __ldg(p.s + m0 + threadIdx.x) : 0.f;
+    const float s_own = threadIdx.x < nrow && m0 + threadIdx.x < p.out ? __ldg(p.s + wrow + m0 + threadIdx.x) : 0.f;
     __syncthreads();
 
     // u is written by the kernel before this one on the stream
@@ -372,7 +402,7 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
                         if (base >= nitems) continue;
                         const int c = base / p.kwc;
                         sm100::tma_load_2d(sm100::smem_addr(stage + (size_t)base * 128), &umap, 0,
-                                           (p.c0 + c) * p.kw + p.kx0 + (base - c * p.kwc), ubar);
+                                           (c0 + c) * p.kw + p.kx0 + (base - c * p.kwc), ubar);
                     }
             } else {
                 sm100::mbar_arrive(ubar);
@@ -458,7 +488,7 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
             const int c = it / p.kwc;
             const int x = p.kx0 + it - c * p.kwc;
             if (it >= nitems || x >= p.kw) return make_float4(0.f, 0.f, 0.f, 0.f);
-            const float* q = p.u + (long long)(p.c0 + c) * p.K + 32 * x + jq;
+            const float* q = p.u + (long long)(c0 + c) * p.K + 32 * x + jq;
             return make_float4(__ldg(q), __ldg(q + 8), __ldg(q + 16), __ldg(q + 24));
         };
         float4 cache[kCached];
@@ -552,8 +582,8 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
         int xs = (tt - gl * tpg) * TS;
         const uint4* bp = bcol + binc * xs;
         const int r0 = m0 + 16 * gl + g, r1 = r0 + 8;
-        const uint32_t* row0 = p.packed + (long long)min(r0, p.out - 1) * p.kw;
-        const uint32_t* row1 = p.packed + (long long)min(r1, p.out - 1) * p.kw;
+        const uint32_t* row0 = p.packed + (wrow + min(r0, p.out - 1)) * p.kw;
+        const uint32_t* row1 = p.packed + (wrow + min(r1, p.out - 1)) * p.kw;
         const bool v0 = r0 < p.out, v1 = r1 < p.out;
         for (; tt < tend; ++tt, xs += TS) {
             uint4 ca0, cb0, ca1 = zero4, cb1 = zero4;
@@ -635,7 +665,7 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
         const ColInfo ci = cinfo[c];
         // sum_k sigma u_q = 2 sum_{bit=1} u_q - sum_k u_q (exact integers)
         const long long sig = 2 * (long long)gacc[item] - ci.sall;
-        const float sr = 16 * gl + row < kThreads ? srow[16 * gl + row] : __ldg(p.s + m);
+        const float sr = 16 * gl + row < kThreads ? srow[16 * gl + row] : __ldg(p.s + wrow + m);
         float res;
         if (ci.mode == kColFinite) {  // undo the 2^F scale
             const double val = (double)sig * __longlong_as_double((long long)(1023 - ci.F) << 52);
@@ -648,17 +678,19 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
             res = __int_as_float(0x7fc00000);
         }
         if constexpr (EPI) {
-            float* part = p.epi.sums + (long long)(p.c0 + c) * p.out + m;
+            float* part = p.epi.sums + (long long)(c0 + c) * p.out + m;
             if (p.accumulate) res += *part;
             if (p.last) {
                 float z[1] = {res};
-                finish_row(p.epi, p.out, p.c0 + c, 1, m, z, lane);
+                DecodeEpilogue epi = p.epi;
+                if (epi.bias) epi.bias += wrow;
+                finish_row(epi, p.out, c0 + c, 1, m, z, lane);
             } else {
                 *part = res;
             }
             continue;
         }
-        float* outp = p.o + (long long)(p.c0 + c) * p.out + m;
+        float* outp = p.o + (long long)(c0 + c) * p.out + m;
         *outp = p.accumulate ? *outp + res : res;
     }
 }
@@ -699,18 +731,18 @@ EncodeTiledFn encode_fn() {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// mma.sync plan: one CTA per SM (or per group when there are fewer groups).
+// mma.sync plan: up to `ctas` CTAs (one per SM, or one per group when there are fewer groups).
 // Preference: up to two columns per pass, then a deep ring (three tiles in
 // flight per warp), then the widest K chunk whose digit planes fit in shared
 // memory (a second launch costs less than a shallow ring: measured).
-bool plan_mma(DecodePlan& pl) {
+bool plan_mma(DecodePlan& pl, int ctas) {
     const int out = pl.out, kw = pl.kw, batch = pl.batch;
     const long long ngroups = ((long long)out + 15) / 16;
     pl.tma = (kw % 4) == 0;
     pl.ts = pl.tma && kw % 16 == 0 ? 2 : 1;
     const int q = pl.ts * kStepWords;  // K chunks hold whole tiles (zeros past the row end)
     const int kwp = (kw + q - 1) / q * q;
-    pl.grid = (int)std::min<long long>(num_sms(), ngroups);
+    pl.grid = (int)std::min<long long>(ctas, ngroups);
     const long long maxgroups = (ngroups + pl.grid - 1) / pl.grid;
     if (maxgroups > (1 << 20)) return false;
     pl.maxgroups = (int)maxgroups;
@@ -755,7 +787,7 @@ cudaError_t launch_kernel(const CUtensorMap& wmap, const CUtensorMap& umap, cons
         if (dev < 64) granted[dev] = pl.smem;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pl.grid, 1, 1);
+    cfg.gridDim = dim3(p.per ? p.per * p.nslots : pl.grid, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = st;
@@ -784,9 +816,13 @@ cudaError_t launch_planned(const CUtensorMap& wmap, const CUtensorMap& umap, boo
     return ustage ? launch_planned_us<true, EPI>(wmap, umap, p, pl, st) : launch_planned_us<false, EPI>(wmap, umap, p, pl, st);
 }
 
+// slots: NULL, or slots of experts in place of one layer's columns (offsets, experts and n of it; pl is the plan
+// of one column on a slot's share of the CTAs).
 cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan& pl, const float* u, float* o,
-                       const DecodeEpilogue* epi, unsigned* status, cudaStream_t st) {
+                       const DecodeEpilogue* epi, const GroupedCall* slots, unsigned* status, cudaStream_t st) {
     const int out = pl.out, kw = pl.kw;
+    const cuuint64_t rows = slots ? (cuuint64_t)slots->experts * out : (cuuint64_t)out;  // of all layers
+    const int columns = slots ? slots->n : pl.batch;
     CUtensorMap wmap, umap;
     memset(&wmap, 0, sizeof(wmap));
     memset(&umap, 0, sizeof(umap));
@@ -796,7 +832,7 @@ cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan&
     if (ustage) {
         EncodeTiledFn encode = encode_fn();
         if (!encode) return cudaErrorNotSupported;
-        cuuint64_t gdim[2] = {32, (cuuint64_t)pl.batch * kw};
+        cuuint64_t gdim[2] = {32, (cuuint64_t)columns * kw};
         cuuint64_t gstride[1] = {128};
         cuuint32_t box[2] = {32, kUBoxRows};
         cuuint32_t estride[2] = {1, 1};
@@ -809,7 +845,7 @@ cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan&
         EncodeTiledFn encode = encode_fn();
         if (!encode) return cudaErrorNotSupported;
         if (pl.ts == 2) {  // [chunk of 16 words][row][word in chunk]: one box = two steps of 16 rows
-            cuuint64_t gdim[3] = {(cuuint64_t)kStepWords, (cuuint64_t)out, (cuuint64_t)(kw / kStepWords)};
+            cuuint64_t gdim[3] = {(cuuint64_t)kStepWords, rows, (cuuint64_t)(kw / kStepWords)};
             cuuint64_t gstride[2] = {(cuuint64_t)kw * 4, (cuuint64_t)kStepWords * 4};
             cuuint32_t box[3] = {kStepWords, 16, 2};
             cuuint32_t estride[3] = {1, 1, 1};
@@ -818,7 +854,7 @@ cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan&
                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
                 return cudaErrorInvalidValue;
         } else {
-            cuuint64_t gdim[2] = {(cuuint64_t)kw, (cuuint64_t)out};
+            cuuint64_t gdim[2] = {(cuuint64_t)kw, rows};
             cuuint64_t gstride[1] = {(cuuint64_t)kw * 4};
             cuuint32_t box[2] = {kStepWords, 16};
             cuuint32_t estride[2] = {1, 1};
@@ -850,6 +886,10 @@ cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan&
             p.accumulate = chunk > 0;
             p.last = chunk + 1 == pl.nchunk;
             p.epi = epi ? *epi : DecodeEpilogue{};
+            p.per = slots ? pl.grid : 0;
+            p.offsets = slots ? slots->offsets : nullptr;
+            p.experts = slots ? slots->experts : 1;
+            p.nslots = slots ? slots->n : 0;
             cudaError_t e = epi ? launch_planned<true>(wmap, umap, ustage, p, pl, st)
                                 : launch_planned<false>(wmap, umap, ustage, p, pl, st);
             if (e != cudaSuccess) return e;
@@ -880,7 +920,7 @@ DecodePlan make_decode_plan(int out, int K, int batch) {
     // its planes fit).
     const double mbytes = (double)out * K / 8 / 1e6;
     pl.tc = (batch >= 4 || (batch == 3 && mbytes >= 40.0)) && plan_tc(pl);
-    if (!pl.tc && !plan_mma(pl) && !(pl.tc = plan_tc(pl))) return pl;
+    if (!pl.tc && !plan_mma(pl, num_sms()) && !(pl.tc = plan_tc(pl))) return pl;
     size_t off = 0;
     if (pl.tc) {
         // column summaries, word info, digit planes, group counters, partial slots
@@ -917,7 +957,7 @@ cudaError_t launch_decode(const DecodePlan& pl, const uint32_t* packed, const fl
         e = launch_quant_mx(u, pl, w, st);
         if (e == cudaSuccess) e = launch_gemv_tc(packed, s, pl, o, epi, w, status, st);
     } else {
-        e = launch_mma(packed, s, pl, u, o, epi, status, st);
+        e = launch_mma(packed, s, pl, u, o, epi, nullptr, status, st);
     }
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
@@ -947,18 +987,40 @@ cudaError_t launch_gemv_epilogue(const uint32_t* packed, const float* s, int out
 
 namespace {
 
-// bf16 u as fp32, eight elements a thread.
-__global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ u, int count, float4* __restrict__ to) {
+// Rows of bf16 u as fp32, eight elements a thread: row i of `to` is row rows[i] (i without rows), zeros for a row outside.
+__global__ void __launch_bounds__(256)
+    widen_kernel(const uint4* __restrict__ u, int tokens, const int* __restrict__ rows, int chunks, float4* __restrict__ to) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the GEMV's weights may be requested meanwhile
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= count) return;
-    const uint4 v = __ldg(u + i);
+    const int x = blockIdx.x * 256 + threadIdx.x, i = blockIdx.y;
+    if (x >= chunks) return;
+    const int row = rows ? __ldg(rows + i) : i;
+    const uint4 zero = {0, 0, 0, 0};
+    const uint4 v = row >= 0 && row < tokens ? __ldg(u + (long long)row * chunks + x) : zero;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[2 * j] = __uint_as_float(w[j] << 16), f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    to[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
-    to[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
+    to += 2 * ((long long)i * chunks + x);
+    to[0] = make_float4(f[0], f[1], f[2], f[3]);
+    to[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+cudaError_t launch_widen(const uint16_t* u, int tokens, const int* rows, int n, int K, float* to, cudaStream_t st) {
+    widen_kernel<<<dim3((K / 8 + 255) / 256, n), 256, 0, st>>>(reinterpret_cast<const uint4*>(u), tokens, rows, K / 8,
+                                                               reinterpret_cast<float4*>(to));
+    return cudaGetLastError();
+}
+
+// The plan of one column on a slot's share of the SMs.
+DecodePlan plan_slots(int out, int K, int n) {
+    DecodePlan pl;
+    memset(&pl, 0, sizeof(pl));
+    pl.out = out;
+    pl.K = K;
+    pl.kw = K / 32;
+    pl.batch = 1;
+    if (n <= num_sms() && plan_mma(pl, num_sms() / n)) pl.bytes = 256;
+    return pl;
 }
 
 size_t widened_bytes(int K, int batch) { return align256((size_t)batch * K * 4); }
@@ -972,14 +1034,28 @@ size_t gemv_epilogue_bf16_workspace_size(int out, int K, int batch) {
 
 cudaError_t launch_gemv_epilogue_bf16(const uint32_t* packed, const float* s, int out, int K, const uint16_t* u, int batch,
                                       const DecodeEpilogue& epi, void* ws, unsigned* status, cudaStream_t st) {
-    const long long count = (long long)batch * K / 8;
     float* wide = static_cast<float*>(ws);
-    widen_kernel<<<(int)((count + 255) / 256), 256, 0, st>>>(reinterpret_cast<const uint4*>(u), (int)count,
-                                                            reinterpret_cast<float4*>(wide));
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_widen(u, batch, nullptr, batch, K, wide, st);
     if (e != cudaSuccess) return e;
     return launch_gemv_epilogue(packed, s, out, K, wide, batch, epi, static_cast<uint8_t*>(ws) + widened_bytes(K, batch), status,
                                 st);
+}
+
+size_t gemv_slots_workspace_size(int out, int K, int n) {
+    const DecodePlan pl = plan_slots(out, K, n);
+    return pl.bytes ? widened_bytes(K, n) + (pl.nchunk > 1 ? align256((size_t)n * out * 4) : 0) : 0;
+}
+
+cudaError_t launch_gemv_slots(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st) {
+    const DecodePlan pl = plan_slots(c.out, c.K, c.n);
+    if (!pl.bytes) return cudaErrorInvalidValue;
+    float* wide = static_cast<float*>(ws);
+    cudaError_t e = launch_widen(c.u, c.tokens, c.rows, c.n, c.K, wide, st);
+    if (e != cudaSuccess) return e;
+    float* sums = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + widened_bytes(c.K, c.n));
+    const DecodeEpilogue epi{c.bias, c.residual, c.o, sums, c.act, c.glu, c.o_bf16};
+    e = launch_mma(c.packed, c.s, pl, wide, nullptr, &epi, &c, status, st);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_lift_gemv(const void* a, bool a_bf16, int batch, int in, const float* tinv, int tblk,

@@ -30,13 +30,24 @@ size_t decode_workspace(const GroupedCall& c) {
     return gemv_epilogue_bf16_workspace_size(c.out, c.K, c.n);
 }
 
-// Up to eight slots an expert, one pass of the mma.sync kernel, which reads the weights once for all of them.
+// Slots of experts that take the same GEMV one by one, a share of the SMs each: up to two an expert, if the shares
+// suffice and rows of words are 16-byte aligned. us against the mma.sync kernel: 2 slots of 8 experts of 11008 x 10240
+// 15 against 27, 16 slots of 16 of 4096 x 10240 29 against 47, 128 of 128 99 against 163; four slots an expert, 16 of 4
+// experts, 28 against 20.
+size_t slots_workspace(const GroupedCall& c) {
+    if (!c.offsets || slots_each(c) > 2 || c.n > 148 || c.K % 128 != 0) return 0;
+    return gemv_slots_workspace_size(c.out, c.K, c.n);
+}
+
+// Up to eight slots an expert, one pass of the mma.sync kernel, which reads the weights once for all of them (us at 8
+// and 9 to 16 tokens of 13824 x 12288: 20 and, in two passes, 38; the tcgen05 kernel 37 for either).
 bool few_rows(const GroupedCall& c) { return slots_each(c) <= 8; }
 
 }  // namespace
 
 size_t grouped_workspace_size(const GroupedCall& c) {
     size_t need = decode_workspace(c);
+    if (!need) need = slots_workspace(c);
     if (!need && !few_rows(c) && c.offsets) need = grouped_tc_workspace_size(c.K, c.n);
     return need > 256 ? need : 256;
 }
@@ -46,6 +57,7 @@ cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cud
         const DecodeEpilogue epi{c.bias, c.residual, c.o, nullptr, c.act, c.glu, c.o_bf16};
         return launch_gemv_epilogue_bf16(c.packed, c.s, c.out, c.K, c.u, c.n, epi, ws, status, st);
     }
+    if (slots_workspace(c)) return launch_gemv_slots(c, ws, status, st);
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

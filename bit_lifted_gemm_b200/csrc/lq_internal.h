@@ -89,6 +89,7 @@ cudaError_t launch_lift_gemv(const void* a, bool a_bf16, int batch, int in, cons
 
 struct DecodePlan;
 struct DecodeEpilogue;
+struct GroupedCall;
 // The quantizers (lq_quant.cu): 32-bit fixed point for the mma.sync kernel
 // (it also clears `nzero` words at `zero`), block-scaled e2m1 digits for the
 // tcgen05 kernel (it also clears the kernel's group counters).
@@ -141,6 +142,11 @@ cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStrea
 // Its kernel for many rows per expert (lq_grouped_tc.cu): bf16 u, about `each` slots to an expert.
 size_t grouped_tc_workspace_size(int K, int n);  // used when rows are given
 cudaError_t launch_grouped_tc(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st, int sms, int each);
+
+// Its path for a few slots, a slot at a time: the decode GEMV with the epilogue on u made fp32, a share of the
+// SMs to each slot (lq_gemv.cu). 0 bytes: no plan fits.
+size_t gemv_slots_workspace_size(int out, int K, int n);
+cudaError_t launch_gemv_slots(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st);
 
 // Rows grouped by expert id, and the experts' rows joined per token (lq_rows.cu).
 cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts, int* offsets, int* rows, int* slots,

@@ -279,6 +279,47 @@ def test_grouped_integer_inputs_are_exact(lq, sizes):
     assert np.array_equal(f64(got), want)
 
 
+@pytest.mark.parametrize("K", [128, 1024, 1152, 4096, 1056])
+@pytest.mark.parametrize("sizes", [[1], [0, 2, 0, 1, 0, 0, 1], [1] * 7 + [0] * 60, [9] + [0] * 40, [0, 70, 0, 3] + [0] * 60])
+def test_grouped_few_slots(lq, sizes, K):
+    """Fewer slots than experts, alone or several in one expert: a share of the SMs to each slot."""
+    rng = np.random.default_rng([22, len(sizes), K])
+    E, out = len(sizes), 150
+    packed, s, offsets, n, rows, u = grouped_case(rng, E, out, K, sizes, True)
+    bias = rng.standard_normal((E, out)).astype(np.float32)
+    for act, glu, o_t in (("gelu", False, "f32"), ("silu", True, "bf16")):
+        got = call_grouped(lq, packed, s, offsets, n, rows, u, bias=bias, act=act, glu=glu, o_dtype=o_t)
+        want, tol, _ = plain.grouped(packed, s.astype(np.float64), u, offsets, n, rows, bias, act, glu)
+        plain.assert_close(f64(got), want, tol, o_t == "bf16")
+
+
+@pytest.mark.parametrize("K", [128, 20480])
+def test_grouped_few_slots_outside(lq, K):
+    """Slots of no expert keep their contents, rows outside u count as zero rows, NaN and Inf stay in their slots."""
+    import torch
+    rng = np.random.default_rng([23, K])
+    E, out, n, tokens = 9, 2050, 6, 4
+    packed, s = make_layer(rng, (E,), out, K)
+    bias = rng.standard_normal((E, out)).astype(np.float32)
+    u = bf16(rng.standard_normal((tokens, K)))
+    u[1, 5], u[2, 7], u[2, 9] = np.nan, np.inf, np.inf
+    rows = np.array([0, 1, 2, 4, -1, 3], np.int32)  # slot 5 belongs to no expert
+    offsets = np.array([0, 0, 1, 3, 3, 3, 4, 5, 5, 5], np.int32)
+    o = torch.full((n, out), 7.5, device="cuda")
+    call_grouped(lq, packed, s, offsets, n, rows, u, bias=bias, out=o)
+    got = f64(o)
+    clean = np.where(np.isfinite(u), u, 0).astype(np.float32)
+    want, tol, written = plain.grouped(packed, s.astype(np.float64), clean, offsets, n, rows, bias)
+    assert written.tolist() == [True] * 5 + [False] and (got[5] == 7.5).all()
+    for i in (0, 3, 4):
+        plain.assert_close(got[i: i + 1], want[i: i + 1], tol[i: i + 1], False)
+    assert np.isnan(got[1]).all()
+    sg = plain.signs(packed[2])
+    opposed = sg[:, 7] != sg[:, 9]
+    assert np.isnan(got[2][opposed]).all()
+    assert np.array_equal(got[2][~opposed], np.where(sg[~opposed, 7] > 0, np.inf, -np.inf))
+
+
 def test_grouped_more_experts_than_a_warp(lq):
     rng = np.random.default_rng(11)
     sizes = rng.integers(0, 4, 300)
