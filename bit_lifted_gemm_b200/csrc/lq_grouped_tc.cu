@@ -3,10 +3,10 @@
 //
 //   z[i][r] = s[r] sum_k sigma[r][k] u[row(i)][k] + bias[r]
 //
-// A unit is a tile of 128 weight rows by up to BN slots of one expert; persistent
-// CTAs (one per SM) take units in turn (256, 128 or 64 slots to a full tile). The MMA's width N is the tile's slots
+// A unit is a tile of 128 weight rows by up to BN slots of one expert (256, 128 or 64);
+// persistent CTAs (one per SM) take units in turn. The MMA's width N is the tile's slots
 // rounded up to 16, so a short tail of an expert costs what it needs. K is walked in
-// steps of 64 (128 for narrow tiles) through a ring of stages. Roles:
+// steps of 64 (128 for the narrowest tiles) through a ring of stages. Roles:
 //   warp 0        u rows of the slots by TMA (128-byte swizzle)
 //   warp 1        issues the MMAs (M = 128, K = 16, bf16, fp32 in TMEM); narrow tiles: warp 14 too
 //   warps 2..9    two groups that fill the stages in turn; a thread owns one weight row, loads its sign
@@ -18,6 +18,12 @@
 // them in this kernel, four to a TMA instruction, took 1200 clocks per 64 k of 256 slots
 // (the MMAs take 512), and with cp.async 1900; the copy costs n K bytes written and read.
 // Products are exact; only the fp32 sums round. Every wait is bounded.
+//
+// What bounds it. Wide tiles: the tensor cores under the power cap (13824 x 12288, 2048 tokens, gated:
+// 427 us = 1630 TFLOP/s in short bursts, 499 us = 1394 of the 1434 TFLOP/s that the library's product
+// sustains). Narrow ones: shared memory, since every sign becomes two bytes that are written and read
+// there: 64 rows by 128 k take 32 + 32 KB for the signs and 16 + 16 KB for u, 768 clocks at 128 bytes
+// each, of the 740 measured (64 tokens 38 us, 128 tokens 56 us).
 #include <cuda.h>
 
 #include "lq_debug.cuh"
@@ -55,6 +61,7 @@ struct Ring {
     static constexpr int A_STAGE = SUB * A_TILE, B_TILE = BN * BK * 2, B_STAGE = SUB * B_TILE;
     static constexpr size_t SMEM_BYTES = 1024 + STAGES * (A_STAGE + B_STAGE) + 256;
 };
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -280,10 +287,9 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
             __syncwarp();
             if (++acc == 2) acc = 0, acc_phase ^= 1;
         }
-        if (lane == 0) {  // no MMA is in flight when TMEM is freed
-            umma_commit(drained);
-            mbar_wait(drained, 0, status);
-        }
+        if (elect_one()) umma_commit(drained);  // no MMA is in flight when TMEM is freed (the issuing lane is always the same)
+        __syncwarp();
+        mbar_wait(drained, 0, status);
     } else if (warp < EPILOGUE_WARP) {
         // ---- signs: each of two groups fills every other stage
         constexpr int WORDS = 2 * SUB, AHEAD = 16 / WORDS;  // sign words of a row and stage; stages loaded ahead

@@ -18,8 +18,9 @@ namespace cg = cooperative_groups;
 // lanes with equal ids find one another by ballots, their lowest lane adds). Prefix sums over the warps,
 // over the cluster's CTAs (distributed shared memory) and over the experts give every warp the
 // first slot of its ids of each expert; walking its run again, it hands them out in order. So
-// slots do not depend on timing and no global scratch is needed. Latency bounds it: loads of
-// eight rounds are issued together, and each round is a chain through shared memory.
+// slots do not depend on timing and no global scratch is needed. Latency bounds it (131072 ids of
+// 128 experts 17.5 us, 90 GB/s; 32 ids 3.9 us): loads of eight rounds are issued together, and each round is a chain
+// of ballots and shared memory.
 constexpr int kMaxWarps = 32, kRounds = 8, kCluster = 16;
 
 // Lanes of the warp with this id (below 2^bits), and this lane's place among them: one ballot a bit. (A match
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 //
 // A thread owns 16 bytes of a token's row (one element where rows are not 16-byte
 // aligned) and adds the token's slots in order, the loads of four issued together. Bound by
-// reading the y rows and writing o.
+// reading the y rows and writing o: 4096 tokens of four slots of 4096 bf16 37.5 us, 5.4 TB/s (83% of the measured copy).
 template <bool BF16, int N>
 struct Chunk {
     typename Elem<BF16>::T v[N];
@@ -218,6 +219,31 @@ cudaError_t launch_combine(const void* y, int n, int width, const int* slots, co
     return cudaGetLastError();
 }
 
+constexpr size_t kGroupSmem = 200 * 1024;
+
+// Whether clusters of sixteen CTAs (more than the portable eight) of the largest size fit on the device.
+signed char sixteen_run(signed char (&known)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return -1;
+    if (known[dev]) return known[dev];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(32 * kMaxWarps);
+    cfg.dynamicSmemBytes = kGroupSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    const bool ok = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGroupSmem) == cudaSuccess &&
+                    cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&clusters, group_kernel, &cfg) == cudaSuccess && clusters > 0;
+    if (!ok) cudaGetLastError();
+    return known[dev] = ok ? 1 : -1;
+}
+
 }  // namespace
 
 cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts, int* offsets, int* rows, int* slots,
@@ -226,7 +252,8 @@ cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts,
     // One CTA up to 512 ids (a cluster's start and two barriers cost more than they save: 32 ids 3.7 us, 2048 ids
     // 8.4 us against 6 for eight CTAs), sixteen from 16384 on (131072 ids: 17.5 us against 28); as many warps
     // as have 64 ids each, and as their counts fit in shared memory
-    const int ctas = n <= 512 ? 1 : n <= 16384 ? 8 : kCluster;
+    static signed char sixteen[64];  // per device: 0 not asked yet, 1 clusters of sixteen run, -1 they do not
+    const int ctas = n <= 512 ? 1 : n <= 16384 || sixteen_run(sixteen) < 0 ? 8 : kCluster;
     const int room = 160 * 1024 / (4 * experts);
     int warps = (n + 64 * ctas - 1) / (64 * ctas);
     warps = warps > kMaxWarps ? kMaxWarps : warps;
@@ -239,8 +266,7 @@ cudaError_t launch_group_rows(const int* ids, int tokens, int topk, int experts,
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaError_t e = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGroupSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }

@@ -345,7 +345,8 @@ def test_outputs_past_32_bit_offsets(lq):
 
 
 @pytest.mark.parametrize("tokens,topk,experts", [(1, 1, 1), (1, 2, 8), (16, 2, 8), (33, 4, 300), (1000, 8, 128), (5, 3, 4096),
-                                                 (4096, 2, 8), (20011, 7, 61), (70000, 2, 5)])
+                                                 (4096, 2, 8), (20011, 7, 61), (70000, 2, 5), (300, 2, 40),
+                                                 (5000, 8, 4096), (2000, 2, 4096)])
 @pytest.mark.parametrize("outside", [False, True])
 def test_group_rows(lq, tokens, topk, experts, outside):
     rng = np.random.default_rng([13, tokens])
