@@ -339,21 +339,33 @@ def _operand(t, name, dtype, shape, device):
     """Address of one operand: a contiguous tensor on CUDA device `device`, of this type and shape; None for None."""
     if t is None:
         return None
-    if t.get_device() != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.get_device() == device and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    raise ValueError(f"{name} must be {dtype} {tuple(shape)} on cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _result(t, name, dtype, shape, like):
+    """(the output given, or a new one beside `like`; its address)."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _operand(t, name, dtype, shape, like.get_device())
+
+
+@functools.lru_cache(maxsize=None)
+def _float_types():
+    import torch
+    f32, bf16 = (torch.float32, LQ_F32), (torch.bfloat16, LQ_BF16)
+    return {"f32": f32, torch.float32: f32, "bf16": bf16, torch.bfloat16: bf16}
 
 
 def _float_type(o_dtype, name="o_dtype"):
-    import torch
-    if o_dtype == "f32" or o_dtype == torch.float32:
-        return torch.float32, LQ_F32
-    if o_dtype == "bf16" or o_dtype == torch.bfloat16:
-        return torch.bfloat16, LQ_BF16
-    raise ValueError(f"{name} must be 'f32' or 'bf16'")
+    found = _float_types().get(o_dtype)
+    if found is None:
+        raise ValueError(f"{name} must be 'f32' or 'bf16'")
+    return found
 
 
 def _activation(act):
@@ -381,14 +393,14 @@ def gemm_grouped_workspace_size(experts: int, out_rows: int, K: int, n: int) -> 
 
 
 def _scratch(ws, need, like):
-    """The workspace given, or a new one beside `like` (the caching allocator aligns to 512 bytes)."""
+    """(the workspace given, or a new one beside `like`; its bytes). The caching allocator aligns to 512 bytes."""
     import torch
     if ws is None:
-        return like.new_empty(need or 1, dtype=torch.uint8)
+        return like.new_empty(need or 1, dtype=torch.uint8), need or 1
     _dev_tensor(ws, "workspace")
     if ws.device != like.device:
         raise ValueError(f"workspace must be on {like.device}")
-    return ws
+    return ws, ws.numel() * ws.element_size()
 
 
 def _layer_epilogue(fn, size_fn, u_type, packed, s, u, bias, act, glu, residual, o_dtype, out, workspace, stream):
@@ -403,16 +415,14 @@ def _layer_epilogue(fn, size_fn, u_type, packed, s, u, bias, act, glu, residual,
     rows, dev = packed.shape[0], u.get_device()
     ot, o_t = _float_type(o_dtype if out is None else out.dtype)
     width = rows // 2 if glu else rows
-    if out is None:
-        out = u.new_empty((tokens, width), dtype=ot)
-    ws = _scratch(workspace, size_fn(rows, K, tokens), u)
+    out, o = _result(out, "out", ot, (tokens, width), u)
+    ws, ws_bytes = _scratch(workspace, size_fn(rows, K, tokens), u)
     f32 = torch.float32
     _check(getattr(lib, fn)(_operand(packed, "packed", torch.int32, (rows, K // 32), dev), _operand(s, "s", f32, (rows,), dev),
                             rows, K, _operand(u, "u", u_type, (tokens, K), dev), tokens,
                             _operand(bias, "bias", f32, (rows,), dev), _activation(act), 1 if glu else 0,
-                            _operand(residual, "residual", ot, (tokens, width), dev),
-                            _operand(out, "out", ot, (tokens, width), dev), o_t, ws.data_ptr(),
-                            ws.numel() * ws.element_size(), _raw_stream(dev)), fn)
+                            _operand(residual, "residual", ot, (tokens, width), dev), o, o_t, ws.data_ptr(), ws_bytes,
+                            _raw_stream(dev)), fn)
     return out
 
 
@@ -458,17 +468,15 @@ def gemm_grouped(packed, s, u, offsets, n, rows=None, bias=None, act=None, glu=F
     n, dev = int(n), u.get_device()
     ot, o_t = _float_type(o_dtype if out is None else out.dtype)
     width = out_rows // 2 if glu else out_rows
-    if out is None:
-        out = u.new_empty((n, width), dtype=ot)
-    ws = _scratch(workspace, gemm_grouped_workspace_size(experts, out_rows, K, n), u)
+    out, o = _result(out, "out", ot, (n, width), u)
+    ws, ws_bytes = _scratch(workspace, gemm_grouped_workspace_size(experts, out_rows, K, n), u)
     f32, i32 = torch.float32, torch.int32
     _check(lib.lq_gemm_grouped(_operand(packed, "packed", i32, (experts, out_rows, K // 32), dev),
                                _operand(s, "s", f32, (experts, out_rows), dev), experts, out_rows, K,
                                _operand(u, "u", torch.bfloat16, (tokens, K), dev), tokens,
                                _operand(rows, "rows", i32, (n,), dev), _operand(offsets, "offsets", i32, (experts + 1,), dev),
                                n, _operand(bias, "bias", f32, (experts, out_rows), dev), _activation(act), 1 if glu else 0,
-                               _operand(out, "out", ot, (n, width), dev), o_t, ws.data_ptr(),
-                               ws.numel() * ws.element_size(), _raw_stream(dev)), "lq_gemm_grouped")
+                               o, o_t, ws.data_ptr(), ws_bytes, _raw_stream(dev)), "lq_gemm_grouped")
     return out
 
 
@@ -485,16 +493,11 @@ def group_rows(expert_ids, experts, offsets=None, rows=None, slots=None, stream=
         raise ValueError("expert_ids must be [tokens][topk]")
     tokens, topk = expert_ids.shape
     dev, i32 = expert_ids.get_device(), torch.int32
-    if offsets is None:
-        offsets = expert_ids.new_empty((experts + 1,))
-    if rows is None:
-        rows = expert_ids.new_empty((tokens * topk,))
-    if slots is None:
-        slots = expert_ids.new_empty((tokens, topk))
+    offsets, offsets_at = _result(offsets, "offsets", i32, (experts + 1,), expert_ids)
+    rows, rows_at = _result(rows, "rows", i32, (tokens * topk,), expert_ids)
+    slots, slots_at = _result(slots, "slots", i32, (tokens, topk), expert_ids)
     _check(lib.lq_group_rows(_operand(expert_ids, "expert_ids", i32, (tokens, topk), dev), tokens, topk, experts,
-                             _operand(offsets, "offsets", i32, (experts + 1,), dev),
-                             _operand(rows, "rows", i32, (tokens * topk,), dev),
-                             _operand(slots, "slots", i32, (tokens, topk), dev), _raw_stream(dev)), "lq_group_rows")
+                             offsets_at, rows_at, slots_at, _raw_stream(dev)), "lq_group_rows")
     return offsets, rows, slots
 
 
@@ -512,13 +515,12 @@ def combine_rows(y, slots, weights, residual=None, out=None, stream=None):
     tokens, topk = slots.shape
     dev = y.get_device()
     yt, y_t = _float_type(y.dtype, "y's type")
-    if out is None:
-        out = y.new_empty((tokens, width))
+    out, o = _result(out, "out", yt, (tokens, width), y)
     _check(lib.lq_combine_rows(_operand(y, "y", yt, (n, width), dev), y_t, n, width,
                                _operand(slots, "slots", torch.int32, (tokens, topk), dev),
                                _operand(weights, "weights", torch.float32, (tokens, topk), dev), tokens, topk,
-                               _operand(residual, "residual", yt, (tokens, width), dev),
-                               _operand(out, "out", yt, (tokens, width), dev), _raw_stream(dev)), "lq_combine_rows")
+                               _operand(residual, "residual", yt, (tokens, width), dev), o, _raw_stream(dev)),
+           "lq_combine_rows")
     return out
 
 
