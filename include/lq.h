@@ -30,7 +30,8 @@
  *  - Debug build: liblq_debug.so, the same entry points compiled with
  *    -DLQ_DEBUG. Its kernels test the element index of each computed global
  *    load and store of the pack, lift, Kronecker lift, prefill GEMM and
- *    encoder kernels against the extent of its buffer (from the call's
+ *    encoder kernels, and of the row operators, the copies of rows and the
+ *    stores of the grouped products, against the extent of its buffer (from the call's
  *    arguments) before the access; a failed test skips the access and latches
  *    LQ_ERR_BOUNDS. Nothing traps. TMA copies are bounded by their tensor maps
  *    in both builds. The release library compiles the tests away.
@@ -303,10 +304,12 @@ typedef enum {
  *              lq_gemm_epilogue_workspace_size(out, K, tokens) bytes; its contents
  *              before the call do not matter. Calls that share one must be ordered.
  *   out >= 1, K >= 32, K % 32 == 0, tokens >= 1
- * Products are exact, sums are fp32, and the result is rounded once, to o's type.
- * A NaN or Inf in a row of u reaches that row of o alone. Every pointer must be
- * memory of the current device. Requires an sm_100 device (else
- * LQ_ERR_UNSUPPORTED). */
+ * Sums are exact or fp32 (one or two tokens, and wide layers at 9 to 16, take the
+ * kernels of lq_gemv with their accuracy), and the result is rounded once, to o's
+ * type. A NaN or Inf in a row of u reaches that row of o alone, as in lq_gemv. Every
+ * pointer must be memory of the current device. In place is refused (residual and o
+ * may not overlap). Bounded waits report LQ_ERR_TIMEOUT through
+ * lq_get_device_status. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
 LQ_API int lq_gemm_epilogue(const uint32_t* packed, const float* s, int out, int K,
                             const uint16_t* u_bf16, int tokens, const float* bias, int act, int glu,
                             const void* residual, void* o, int o_dtype,
@@ -315,9 +318,11 @@ LQ_API int lq_gemm_epilogue(const uint32_t* packed, const float* s, int out, int
 /* Bytes of workspace lq_gemm_epilogue needs; 0 for sizes it refuses. Host only. */
 LQ_API size_t lq_gemm_epilogue_workspace_size(int out, int K, int tokens);
 
-/* The same epilogue for decode with fp32 u [batch][K], batch 1..16, at fp32
- * accuracy (no rounding of u to 16 bits). Arguments as lq_gemm_epilogue;
- * workspace of lq_gemv_epilogue_workspace_size(out, K, batch) bytes. */
+/* The same epilogue for decode with fp32 u [batch][K], batch 1..16: lq_gemv's
+ * kernels, accuracy, limits on out and programmatic launch (packed and s may be read
+ * before the kernel before it on the stream completes; u, bias and residual are not).
+ * Arguments as lq_gemm_epilogue; workspace of
+ * lq_gemv_epilogue_workspace_size(out, K, batch) bytes. */
 LQ_API int lq_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K,
                             const float* u, int batch, const float* bias, int act, int glu,
                             const void* residual, void* o, int o_dtype,
@@ -343,8 +348,10 @@ LQ_API size_t lq_gemv_epilogue_workspace_size(int out, int K, int batch);
  *   o       : [n][width], o_dtype; only slots of some expert are written
  *   workspace: lq_gemm_grouped_workspace_size(experts, out, K, n) bytes, as above
  *   experts 1..4096, experts*out below 2^31, tokens >= 1, n >= 1
- * A slot's result does not depend on which other slots are in the call's groups
- * beyond fp32 rounding. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
+ * Kernels are chosen by n / min(n, experts), the slots of an expert if they spread
+ * evenly; any sizes are right, very uneven ones slower. A slot's result does not
+ * depend on the other slots of the call. Requires an sm_100 device (else
+ * LQ_ERR_UNSUPPORTED). */
 LQ_API int lq_gemm_grouped(const uint32_t* packed, const float* s, int experts, int out, int K,
                            const uint16_t* u_bf16, int tokens, const int* rows, const int* offsets, int n,
                            const float* bias, int act, int glu, void* o, int o_dtype,
