@@ -253,7 +253,11 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
     long long wrow = 0;                                 // first weight row of the layer
     if (EPI && p.per) {
         const int slot = cta / p.per, e = expert_of(p.offsets, p.experts, p.nslots, slot, lane);
-        if (e < 0) return;  // a slot of no expert: the whole CTA
+        if (e < 0) {  // a slot of no expert: the whole CTA, but not before the kernels ahead are through, which the
+            // kernels behind this one take for granted
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            return;
+        }
         cta -= slot * p.per;
         ctas = p.per;
         c0 = slot;

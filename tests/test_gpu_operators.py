@@ -269,6 +269,26 @@ def test_grouped_nothing_routed(lq):
     assert bool((out_t == 2.0).all())
 
 
+def test_grouped_calls_without_slots_leave_the_next_call_alone(lq):
+    """On one workspace: what calls without any slot prepare there must not come after what a call with slots does."""
+    import torch
+    rng = np.random.default_rng(24)
+    E, out, K, n = 4, 256, 40960, 4
+    packed, s, offsets, _, rows, u = grouped_case(rng, E, out, K, [1] * 4, True)
+    weights = dev(packed), gpu(s)
+    other, here = gpu(-u, True), gpu(u, True)
+    none, each, at = ints(np.zeros(E + 1)), ints(offsets), ints(rows)
+    alone = lq.gemm_grouped(*weights, here, each, n, rows=at)
+    ws = torch.empty(lq.gemm_grouped_workspace_size(E, out, K, n), dtype=torch.uint8, device="cuda")
+    unused = torch.full((n, out), 7.5, device="cuda")
+    for _ in range(50):
+        for _ in range(3):
+            lq.gemm_grouped(*weights, other, none, n, rows=at, out=unused, workspace=ws)
+        got = lq.gemm_grouped(*weights, here, each, n, rows=at, workspace=ws)
+        assert torch.equal(got, alone)
+    assert bool((unused == 7.5).all())
+
+
 @pytest.mark.parametrize("sizes", [[3, 0, 9, 1], [30, 70, 5, 250]])
 def test_grouped_integer_inputs_are_exact(lq, sizes):
     rng = np.random.default_rng(10)
