@@ -479,13 +479,18 @@ lq::GroupedCall sized_call(int experts, int out, int K, int n) {
     return c;
 }
 
-bool layer_sizes_ok(int out, int K) { return out >= 1 && K >= 32 && K % 32 == 0; }
-
+// Counts of rows, slots, columns and ids: 4096 below 2^31, so that the kernels' 32-bit counters may step past the end by a
+// tile or by a grid.
+constexpr long long kMaxCount = 0x7fffffffLL - 4096;
 constexpr int kMaxExperts = 4096;
 
+bool count_ok(long long x) { return x >= 1 && x <= kMaxCount; }
+
+bool layer_sizes_ok(int out, int K) { return count_ok(out) && K >= 32 && K % 32 == 0 && count_ok(K); }
+
 bool grouped_sizes_ok(int experts, int out, int K, int n) {
-    return layer_sizes_ok(out, K) && experts >= 1 && experts <= kMaxExperts && n >= 1 &&
-           (long long)experts * out <= 0x7fffffffLL;
+    return layer_sizes_ok(out, K) && experts >= 1 && experts <= kMaxExperts && count_ok(n) &&
+           count_ok((long long)experts * out);
 }
 
 }  // namespace
@@ -493,14 +498,14 @@ bool grouped_sizes_ok(int experts, int out, int K, int n) {
 extern "C" {
 
 size_t lq_gemm_epilogue_workspace_size(int out, int K, int tokens) {
-    if (!layer_sizes_ok(out, K) || tokens < 1) return 0;
+    if (!layer_sizes_ok(out, K) || !count_ok(tokens)) return 0;
     return lq::grouped_workspace_size(sized_call(1, out, K, tokens));
 }
 
 int lq_gemm_epilogue(const uint32_t* packed, const float* s, int out, int K, const uint16_t* u_bf16, int tokens,
                      const float* bias, int act, int glu, const void* residual, void* o, int o_dtype, void* workspace,
                      size_t workspace_bytes, void* stream) {
-    if (!layer_sizes_ok(out, K) || tokens < 1) return LQ_ERR_INVALID_ARG;
+    if (!layer_sizes_ok(out, K) || !count_ok(tokens)) return LQ_ERR_INVALID_ARG;
     return grouped_call(layer_call(packed, s, out, K, u_bf16, tokens, bias, act, glu, residual, o, o_dtype),
                         o_dtype, glu, workspace, workspace_bytes, stream);
 }
@@ -537,7 +542,7 @@ size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n) {
 int lq_gemm_grouped(const uint32_t* packed, const float* s, int experts, int out, int K, const uint16_t* u_bf16,
                     int tokens, const int* rows, const int* offsets, int n, const float* bias, int act, int glu,
                     void* o, int o_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    if (!grouped_sizes_ok(experts, out, K, n) || tokens < 1 || !offsets) return LQ_ERR_INVALID_ARG;
+    if (!grouped_sizes_ok(experts, out, K, n) || !count_ok(tokens) || !offsets) return LQ_ERR_INVALID_ARG;
     if (!rows && tokens < n) return LQ_ERR_INVALID_ARG;
     lq::GroupedCall c = layer_call(packed, s, out, K, u_bf16, tokens, bias, act, glu, nullptr, o, o_dtype);
     c.experts = experts;
@@ -551,7 +556,7 @@ int lq_group_rows(const int* expert_ids, int tokens, int topk, int experts, int*
                   void* stream) {
     if (!expert_ids || !offsets || !rows || !slots || !all_aligned16({expert_ids, offsets, rows, slots}))
         return LQ_ERR_INVALID_ARG;
-    if (tokens < 1 || topk < 1 || experts < 1 || experts > kMaxExperts || (long long)tokens * topk > 0x7fffffffLL)
+    if (tokens < 1 || topk < 1 || experts < 1 || experts > kMaxExperts || !count_ok((long long)tokens * topk))
         return LQ_ERR_INVALID_ARG;
     const size_t each = nbytes((long long)tokens * topk, 4);
     if (aliased({{expert_ids, each, false},
@@ -572,7 +577,7 @@ int lq_combine_rows(const void* y, int dtype, int n, int width, const int* slots
                     int topk, const void* residual, void* o, void* stream) {
     if (!y || !slots || !weights || !o || !all_aligned16({y, slots, weights, residual, o})) return LQ_ERR_INVALID_ARG;
     if (dtype != LQ_F32 && dtype != LQ_BF16) return LQ_ERR_INVALID_ARG;
-    if (n < 1 || width < 1 || tokens < 1 || topk < 1 || (long long)tokens * topk > 0x7fffffffLL)
+    if (!count_ok(n) || !count_ok(width) || tokens < 1 || topk < 1 || !count_ok((long long)tokens * topk))
         return LQ_ERR_INVALID_ARG;
     const size_t e = dtype == LQ_BF16 ? 2 : 4;
     if (aliased({{y, nbytes((long long)n * width, e), false},

@@ -303,7 +303,7 @@ typedef enum {
  *   workspace: 256-byte aligned device memory of at least
  *              lq_gemm_epilogue_workspace_size(out, K, tokens) bytes; its contents
  *              before the call do not matter. Calls that share one must be ordered.
- *   out >= 1, K >= 32, K % 32 == 0, tokens >= 1
+ *   out >= 1, K >= 32, K % 32 == 0, tokens >= 1, none above 2^31 - 4097
  * Sums are exact or fp32 (one or two tokens, and wide layers at 9 to 16, take the
  * kernels of lq_gemv with their accuracy), and the result is rounded once, to o's
  * type. A NaN or Inf in a row of u reaches that row of o alone, as in lq_gemv. Every
@@ -347,7 +347,7 @@ LQ_API size_t lq_gemv_epilogue_workspace_size(int out, int K, int batch);
  *   bias    : fp32 [experts][out] or NULL
  *   o       : [n][width], o_dtype; only slots of some expert are written
  *   workspace: lq_gemm_grouped_workspace_size(experts, out, K, n) bytes, as above
- *   experts 1..4096, experts*out below 2^31, tokens >= 1, n >= 1
+ *   experts 1..4096, tokens >= 1, n >= 1; experts*out, K, tokens and n up to 2^31 - 4097
  * Kernels are chosen by n / min(n, experts), the slots of an expert if they spread
  * evenly; any sizes are right, very uneven ones slower. A slot's result does not
  * depend on the other slots of the call. Requires an sm_100 device (else
@@ -369,7 +369,7 @@ LQ_API size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n)
  *                offsets[experts] on
  *   slots      : int32 [tokens][topk] (written): the slot of each pair, -1 if left out
  * Within an expert slots follow (token, choice) order, so the result is unique.
- * tokens >= 1, topk >= 1, tokens*topk below 2^31, experts 1..4096; int32 arrays 16-byte
+ * tokens >= 1, topk >= 1, tokens*topk up to 2^31 - 4097, experts 1..4096; int32 arrays 16-byte
  * aligned like every tensor. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
 LQ_API int lq_group_rows(const int* expert_ids, int tokens, int topk, int experts, int* offsets,
                          int* rows, int* slots, void* stream);
@@ -383,7 +383,7 @@ LQ_API int lq_group_rows(const int* expert_ids, int tokens, int topk, int expert
  *   residual : [tokens][width] of the same dtype, or NULL
  *   o        : [tokens][width] of the same dtype (written); a token with no slot
  *              gets its residual, or zeros
- * n, width, tokens, topk >= 1. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
+ * n, width, tokens, topk >= 1; n, width and tokens*topk up to 2^31 - 4097. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */
 LQ_API int lq_combine_rows(const void* y, int dtype, int n, int width, const int* slots, const float* weights,
                            int tokens, int topk, const void* residual, void* o, void* stream);
 

@@ -42,6 +42,13 @@ BAD += [("lq_gemv_epilogue", {"tokens": 17}), ("lq_gemm_grouped", {"experts": 0}
         ("lq_combine_rows", {"width": 0}), ("lq_combine_rows", {"tokens": 0}), ("lq_combine_rows", {"topk": 0}),
         ("lq_combine_rows", {"tokens": 1 << 20, "topk": 1 << 12})]
 
+LAST, PAST = 2 ** 31 - 4097, 2 ** 31 - 4096  # the largest count that is taken, and the next one
+BAD += [("lq_gemm_epilogue", {"out": PAST, "K": 32}), ("lq_gemm_epilogue", {"K": PAST}), ("lq_gemm_epilogue", {"tokens": PAST}),
+        ("lq_gemv_epilogue", {"K": PAST}), ("lq_gemm_grouped", {"experts": 1, "out": PAST}), ("lq_gemm_grouped", {"n": PAST}),
+        ("lq_gemm_grouped", {"experts": 4096, "out": 2 ** 19}), ("lq_gemm_grouped", {"tokens": PAST}),
+        ("lq_group_rows", {"tokens": 1, "topk": PAST}), ("lq_group_rows", {"tokens": PAST, "topk": 1}),
+        ("lq_combine_rows", {"tokens": 1, "topk": PAST}), ("lq_combine_rows", {"n": PAST}), ("lq_combine_rows", {"width": PAST})]
+
 
 def call(fn, **change):
     import bit_lifted_gemm_b200 as lq
@@ -65,6 +72,16 @@ def test_good_arguments_pass_the_checks(fn, monkeypatch):
     if fn == "lq_gemm_grouped":
         change["tokens"] = 8
     assert call(fn, **change) == lq.LQ_ERR_CUDA
+
+
+@pytest.mark.parametrize("fn,change", [("lq_gemm_grouped", {"tokens": LAST, "K": 32, "out": 2}), ("lq_group_rows", {"tokens": 1, "topk": LAST}),
+                                       ("lq_combine_rows", {"tokens": 1, "topk": LAST}), ("lq_combine_rows", {"n": 1, "width": LAST, "tokens": 1})])
+def test_largest_counts_pass_the_checks(fn, change, monkeypatch):
+    import bit_lifted_gemm_b200 as lq
+    monkeypatch.setenv("LQ_FAULT", "launch")
+    # one TiB between the buffers
+    apart = {k: ctypes.c_void_p((i + 1) << 40) for i, (k, v) in enumerate(BASE[fn].items()) if isinstance(v, ctypes.c_void_p)}
+    assert call(fn, **apart, **change) == lq.LQ_ERR_CUDA
 
 
 @pytest.mark.parametrize("fn,outputs", [("lq_gemm_epilogue", ["o", "workspace"]), ("lq_gemv_epilogue", ["o", "workspace"]),
