@@ -66,6 +66,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "lq_decode.h"
 #include "lq_epilogue.cuh"
@@ -187,9 +188,14 @@ struct GemvArgs {
     int pitch;        // chunks per shared-memory digit plane
     unsigned image_bytes;
     int accumulate;   // 1: o += this launch's result
-    int last;         // 1: no launch over K follows for these columns
+};
+
+// What the kernel with the epilogue takes besides. (In the plain kernel's arguments they made it 3 to 7% slower:
+// 10.85 us in place of 10.47 for 13824 x 12288.)
+struct GemvEpiArgs : GemvArgs {
+    int last;  // 1: no launch over K follows for these columns
     DecodeEpilogue epi;
-    // slots of experts (EPI): slot i, row i of u and of o, is contracted by CTAs [i * per, (i + 1) * per) with the layer of the
+    // slots of experts: slot i, row i of u and of o, is contracted by CTAs [i * per, (i + 1) * per) with the layer of the
     // expert whose range holds it; packed, s and bias hold all experts' rows
     int per;             // 0: one layer
     const int* offsets;  // [experts + 1]
@@ -238,7 +244,7 @@ __host__ __device__ inline Layout gemv_layout(int ts, int stages, bool tma, bool
 template <int TS, int STAGES, bool TMA, bool USTAGE, bool EPI>
 __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift beside it
     gemv_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap umap,
-                const GemvArgs p) {
+                const std::conditional_t<EPI, GemvEpiArgs, GemvArgs> p) {
     // a dependent launch (the next K chunk or column pass) may be scheduled as
     // SMs free up; it reads o only after its own griddepcontrol.wait, which
     // waits for this grid to complete
@@ -249,19 +255,22 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
     uint8_t* smem = smem_raw + ((1024u - (sm100::smem_addr(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    int cta = blockIdx.x, ctas = gridDim.x, c0 = p.c0;  // this CTA's place, and the first column
-    long long wrow = 0;                                 // first weight row of the layer
-    if (EPI && p.per) {
-        const int slot = cta / p.per, e = expert_of(p.offsets, p.experts, p.nslots, slot, lane);
-        if (e < 0) {  // a slot of no expert: the whole CTA, but not before the kernels ahead are through, which the
-            // kernels behind this one take for granted
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            return;
+    unsigned cta = blockIdx.x, ctas = gridDim.x;  // this CTA's place
+    int c0 = p.c0;                                // first column
+    long long wrow = 0;                           // first weight row of the layer
+    if constexpr (EPI) {
+        if (p.per) {
+            const int slot = cta / p.per, e = expert_of(p.offsets, p.experts, p.nslots, slot, lane);
+            if (e < 0) {  // a slot of no expert: the whole CTA, but not before the kernels ahead are through, which the
+                // kernels behind this one take for granted
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                return;
+            }
+            cta -= slot * p.per;
+            ctas = p.per;
+            c0 = slot;
+            wrow = (long long)e * p.out;
         }
-        cta -= slot * p.per;
-        ctas = p.per;
-        c0 = slot;
-        wrow = (long long)e * p.out;
     }
     const int gbeg = split_point(cta, p.ngroups, ctas);
     const int gend = split_point(cta + 1, p.ngroups, ctas);
@@ -787,16 +796,17 @@ bool plan_mma(DecodePlan& pl, int ctas) {
 }
 
 template <int TS, int STAGES, bool TMA, bool USTAGE, bool EPI>
-cudaError_t launch_kernel(const CUtensorMap& wmap, const CUtensorMap& umap, const GemvArgs& p, const DecodePlan& pl,
+cudaError_t launch_kernel(const CUtensorMap& wmap, const CUtensorMap& umap, const GemvEpiArgs& p, const DecodePlan& pl,
                           cudaStream_t st) {
     auto kern = gemv_kernel<TS, STAGES, TMA, USTAGE, EPI>;
-    static size_t granted[64] = {};
+    // the limit of all plans at once: of two calls at the same time none lowers it again
+    static bool granted[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev >= 64 || granted[dev] < pl.smem) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem);
+    if (dev >= 64 || !granted[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBudget);
         if (e != cudaSuccess) return e;
-        if (dev < 64) granted[dev] = pl.smem;
+        if (dev < 64) granted[dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.per ? p.per * p.nslots : pl.grid, 1, 1);
@@ -808,11 +818,11 @@ cudaError_t launch_kernel(const CUtensorMap& wmap, const CUtensorMap& umap, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, wmap, umap, p);
+    return cudaLaunchKernelEx(&cfg, kern, wmap, umap, static_cast<const std::conditional_t<EPI, GemvEpiArgs, GemvArgs>&>(p));
 }
 
 template <bool US, bool EPI>
-cudaError_t launch_planned_us(const CUtensorMap& wmap, const CUtensorMap& umap, const GemvArgs& p,
+cudaError_t launch_planned_us(const CUtensorMap& wmap, const CUtensorMap& umap, const GemvEpiArgs& p,
                               const DecodePlan& pl, cudaStream_t st) {
     if (pl.ts == 2)
         return pl.stages == 4 ? launch_kernel<2, 4, true, US, EPI>(wmap, umap, p, pl, st)
@@ -822,7 +832,7 @@ cudaError_t launch_planned_us(const CUtensorMap& wmap, const CUtensorMap& umap, 
 }
 
 template <bool EPI>
-cudaError_t launch_planned(const CUtensorMap& wmap, const CUtensorMap& umap, bool ustage, const GemvArgs& p,
+cudaError_t launch_planned(const CUtensorMap& wmap, const CUtensorMap& umap, bool ustage, const GemvEpiArgs& p,
                            const DecodePlan& pl, cudaStream_t st) {
     if (!pl.tma) return launch_kernel<1, 4, false, false, EPI>(wmap, umap, p, pl, st);
     return ustage ? launch_planned_us<true, EPI>(wmap, umap, p, pl, st) : launch_planned_us<false, EPI>(wmap, umap, p, pl, st);
@@ -878,7 +888,7 @@ cudaError_t launch_mma(const uint32_t* packed, const float* s, const DecodePlan&
     }
     for (int pass = 0; pass < pl.npass; ++pass) {
         for (int chunk = 0; chunk < pl.nchunk; ++chunk) {
-            GemvArgs p;
+            GemvEpiArgs p;
             p.packed = packed;
             p.s = s;
             p.o = o;

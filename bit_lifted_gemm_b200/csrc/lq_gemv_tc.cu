@@ -65,6 +65,7 @@ constexpr int kMaxSA = 4;                           // tensor-memory A / scale s
 constexpr int kWTile = 128 * kStageW * 4;           // sign words of one M-tile in a stage: 16 KB
 constexpr int kSFCols = 16;                         // TMEM columns of a slot's B scales (4 per MMA)
 constexpr uint32_t kSpin = 1000000000u;             // bounded waits: 1 s
+constexpr size_t kSmemLimit = 227 * 1024;           // shared memory of a CTA
 
 constexpr int kExpWarps = 8;                        // sign expansion: two warps per TMEM lane quarter
 
@@ -738,7 +739,7 @@ bool plan_tc(DecodePlan& p) {
     // shared memory: as many stages as fit, up to kMaxSS
     p.tc_nss = 0;
     for (int nss = kMaxSS; nss >= 2; --nss)
-        if (tc_smem(p.tc_mt, p.tc_n, p.batch, nss).total <= 227 * 1024) {
+        if (tc_smem(p.tc_mt, p.tc_n, p.batch, nss).total <= kSmemLimit) {
             p.tc_nss = nss;
             break;
         }
@@ -836,14 +837,14 @@ cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodeP
 
     auto kern = epi ? (pl.tc_mt == 4 ? gemv_tc_kernel<4, true> : gemv_tc_kernel<2, true>)
                     : (pl.tc_mt == 4 ? gemv_tc_kernel<4, false> : gemv_tc_kernel<2, false>);
-    static size_t granted[4][64] = {};
+    static bool granted[4][64] = {};  // the limit of all plans, as in lq_gemv.cu
     int dev = 0;
     cudaGetDevice(&dev);
     const int ki = (pl.tc_mt == 4 ? 1 : 0) + (epi ? 2 : 0);
-    if (dev >= 64 || granted[ki][dev] < pl.tc_smem) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.tc_smem);
+    if (dev >= 64 || !granted[ki][dev]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
         if (e != cudaSuccess) return e;
-        if (dev < 64) granted[ki][dev] = pl.tc_smem;
+        if (dev < 64) granted[ki][dev] = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pl.tc_grid, 1, 1);

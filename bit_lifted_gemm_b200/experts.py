@@ -48,7 +48,12 @@ class ExpertMLP:
 
         Nothing is read back to the host, so the step can be captured in a CUDA graph. Ids
         outside 0..experts-1 are skipped."""
+        import torch
         from . import _on, combine_rows, gemm_grouped, group_rows, lift_activations
+        if x.dim() != 2 or x.shape[1] != self.model or expert_ids.dim() != 2 or expert_ids.shape[0] != x.shape[0]:
+            raise ValueError(f"x must be [tokens][{self.model}] and expert_ids [tokens][topk]")
+        if weights.shape != expert_ids.shape or x.dtype != torch.bfloat16:
+            raise ValueError("x must be bfloat16 and weights [tokens][topk]")
         n = expert_ids.numel()
         with _on(x, stream):
             u = lift_activations(x, self.M, self.K1, tinv=self.tinv_in, u_dtype="bf16")

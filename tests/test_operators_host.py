@@ -152,5 +152,11 @@ def test_experts_block_checks_its_widths():
         interleave_rows(gate, up[:, :4])
     M = torch.zeros((10, 24))
     s = torch.zeros((2, 16))
+    block = ExpertMLP(torch.zeros((2, 20, 3), dtype=torch.int32), torch.zeros((2, 20)),
+                      torch.zeros((2, 40, 1), dtype=torch.int32), torch.zeros((2, 40)), M)
+    x, ids, w = torch.zeros((5, 40), dtype=torch.bfloat16), torch.zeros((5, 2), dtype=torch.int32), torch.zeros((5, 2))
+    for bad in ((x[:4], ids, w), (x, ids, w[:4]), (x, ids[:, 0], w[:, 0]), (x[:, :32], ids, w), (x.float(), ids, w)):
+        with pytest.raises(ValueError, match="must be"):
+            block.step(*bad)
     with pytest.raises(ValueError):  # model = 40 channels lift to 96 columns = 3 words, hidden = 8 is no multiple of d
         ExpertMLP(both, s, torch.zeros((2, 40, 1), dtype=torch.int32), s, M)
