@@ -52,7 +52,7 @@ constexpr int kUPitch = kRunK * 2 + 16;      // bytes of one u row of a stage: 1
 constexpr int kMaxStages = 16;
 constexpr size_t kSmemMax = 227 * 1024 - 2048;
 static_assert(kProducers % 2 == 0, "stages in rounds of the producers are whole rounds of the two groups");
-constexpr size_t kHead = 512 + 1024 + 512;  // barriers, a block's scales and biases, zeros
+constexpr size_t kHead = 512 + 512;  // barriers, zeros
 
 constexpr int COLS = 8, H = 8;  // columns of a pass, tiles of 16 rows that a block may have
 // Two groups of consumers: a third (registers moved over from the other warps) changed no time by more than 2%.
@@ -132,14 +132,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t full0 = smem_addr(tail), empty0 = full0 + 8 * kMaxStages;
     const uint32_t red_full = full0 + 16 * kMaxStages, red_empty = red_full + 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 16 * kMaxStages + 16);
-    float* scale = reinterpret_cast<float*>(tail + 512);  // [128], and the biases
-    float* shift = scale + 128;
-    const uint32_t zeros = smem_addr(tail + 1536);
+    const uint32_t zeros = smem_addr(tail + 512);
     float* red = reinterpret_cast<float*>(tail + kHead);  // [consumers][COLS][rp]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kw = c.K >> 5, runs = (kw + kRunWords - 1) / kRunWords;
 
-    if (threadIdx.x < 128) reinterpret_cast<uint32_t*>(tail + 1536)[threadIdx.x] = 0;
+    if (threadIdx.x < 128) reinterpret_cast<uint32_t*>(tail + 512)[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(full0 + 8 * i, 32 + (TMA ? 1 : 0));
@@ -164,61 +162,55 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     if (warp >= EPILOGUE) {
         // ---- epilogue of a block, while the consumers are at the next one: the warps' sums in warp order
-        const int step = c.glu ? 2 : 1, width = c.glu ? c.out / 2 : c.out;
+        // A thread owns one output row of the block (a pair of weight rows when gated) and every per-th slot of the pass.
+        const int step = c.glu ? 2 : 1, width = c.glu ? c.out / 2 : c.out, tid = threadIdx.x - 32 * EPILOGUE;
         for (long long unit = blockIdx.x; walk.find<true>(c, COLS, p.nblk, unit, lane, u); unit += gridDim.x) {
             int tile0;
-            const int h = block_tiles(p, u.blk, tile0), per_col = 16 * h / step;
-            // the rows' scales and biases, one row to a thread, before the sums are there
-            const int tid = threadIdx.x - 32 * EPILOGUE;
-            if (tid < 16 * h) {
-                const int row = min(16 * tile0 + tid, c.out - 1);
-                const long long at = (long long)u.e * c.out + row;
-                scale[tid] = __ldg(c.s + at);
-                shift[tid] = c.bias ? __ldg(c.bias + at) : 0.f;
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int h = block_tiles(p, u.blk, tile0), outputs = 16 * h / step, per = 128 / outputs;
+            const int first = tid / outputs, r = (tid - first * outputs) * step, row = 16 * tile0 + r;
+            const bool mine = first < per && row < c.out;
+            float scale[2] = {0.f, 0.f}, shift[2] = {0.f, 0.f};  // before the sums are there
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (mine && i < step) {
+                    const long long at = (long long)u.e * c.out + row + i;
+                    scale[i] = __ldg(c.s + at);
+                    if (c.bias) shift[i] = __ldg(c.bias + at);
+                }
             if (!mbar_try_wait(red_full, phase) && !*abort_flag && !mbar_wait(red_full, phase, status)) *abort_flag = 1;
-            if (!*abort_flag) {
-                constexpr int MANY = 4;  // outputs of a thread at a time
-                const int count = u.slots * per_col;
-                for (int x0 = tid; x0 < count; x0 += 128 * MANY) {
-                    float y[MANY], res[MANY];
-                    long long at[MANY];
+            constexpr int MANY = 4;  // outputs of a thread at a time
+            for (int slot0 = first; mine && slot0 < u.slots && !*abort_flag; slot0 += MANY * per) {
+                float y[MANY], other[MANY], res[MANY];
+                const long long at0 = (long long)(u.slot0 + slot0) * width + row / step, at_step = (long long)per * width;
 #pragma unroll
-                    for (int m = 0; m < MANY; ++m) {
-                        const int x = x0 + 128 * m;
-                        const int slot = x / per_col, row = 16 * tile0 + (x - slot * per_col) * step;
-                        at[m] = x < count && row < c.out ? (long long)(u.slot0 + slot) * width + row / step : -1;
-                        res[m] = c.residual && at[m] >= 0 ? load_elem(c.residual, at[m], c.o_bf16) : 0.f;
-                    }
+                for (int m = 0; m < MANY; ++m) {
+                    const int slot = slot0 + m * per;
+                    const bool there = slot < u.slots;
+                    res[m] = there && c.residual ? load_elem(c.residual, at0 + m * at_step, c.o_bf16) : 0.f;
+                    float z[2] = {0.f, 0.f};
+                    const float* sums = red + (there ? slot : slot0) * p.rp + r;
+                    if (c.glu) {
 #pragma unroll
-                    for (int m = 0; m < MANY; ++m) {
-                        const int x = x0 + 128 * m;
-                        if (x >= count) break;
-                        const int slot = x / per_col, r = (x - slot * per_col) * step;
-                        float z[2] = {0.f, 0.f};
-                        const float* sums = red + slot * p.rp + r;
-                        if (c.glu) {
-#pragma unroll
-                            for (int w = 0; w < CONSUMERS; ++w) {
-                                const float2 v = *reinterpret_cast<const float2*>(sums + w * COLS * p.rp);
-                                z[0] += v.x, z[1] += v.y;
-                            }
-                        } else {
-#pragma unroll
-                            for (int w = 0; w < CONSUMERS; ++w) z[0] += sums[w * COLS * p.rp];
+                        for (int w = 0; w < CONSUMERS; ++w) {
+                            const float2 v = *reinterpret_cast<const float2*>(sums + w * COLS * p.rp);
+                            z[0] += v.x, z[1] += v.y;
                         }
-                        z[0] = scale[r] * z[0] + shift[r];
-                        y[m] = activate(z[0], c.act);
-                        if (c.glu) y[m] *= scale[r + 1] * z[1] + shift[r + 1];
-                    }
+                    } else {
 #pragma unroll
-                    for (int m = 0; m < MANY; ++m)
-                        if (at[m] >= 0 && LQ_IN_BOUNDS(at[m], (long long)c.n * width))
-                            store_elem(c.o, at[m], c.o_bf16, c.residual ? y[m] + res[m] : y[m]);
+                        for (int w = 0; w < CONSUMERS; ++w) z[0] += sums[w * COLS * p.rp];
+                    }
+                    y[m] = scale[0] * z[0] + shift[0];
+                    other[m] = scale[1] * z[1] + shift[1];
+                }
+                activate_all(y, c.act);
+#pragma unroll
+                for (int m = 0; m < MANY; ++m) {
+                    if (c.glu) y[m] *= other[m];
+                    if (c.residual) y[m] += res[m];
+                    if (slot0 + m * per < u.slots && LQ_IN_BOUNDS(at0 + m * at_step, (long long)c.n * width))
+                        store_elem(c.o, at0 + m * at_step, c.o_bf16, y[m]);
                 }
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // scale and shift are free again
             __syncwarp();
             if (lane == 0) mbar_arrive(red_empty);
             phase ^= 1;
