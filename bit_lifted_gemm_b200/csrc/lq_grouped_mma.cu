@@ -99,7 +99,8 @@ __device__ __forceinline__ bool elect_one() {
 struct Plan {
     uint32_t shift[16];  // 2^(15 - j): kept from the compiler, so that it multiplies (see sign_pair)
     int stages, stage_bytes, rp;    // rp: pitch of a column of the warps' sums, in floats
-    int nblk, tiles, hmax;          // blocks and tiles of an expert's rows; a block has hmax tiles or one less
+    int nblk, hmax;                 // blocks of an expert's rows; a block has hmax tiles or one less
+    int tall, low;                  // the first `tall` blocks have low + 1 tiles, the others low
     size_t smem;
 };
 
@@ -116,8 +117,8 @@ __device__ __forceinline__ uint32_t sign_pair(uint32_t w, const Plan& p, int j) 
 
 // First tile and number of tiles of block blk: the tiles cut evenly.
 __device__ __forceinline__ int block_tiles(const Plan& p, int blk, int& tile0) {
-    tile0 = (int)((long long)blk * p.tiles / p.nblk);
-    return (int)((long long)(blk + 1) * p.tiles / p.nblk) - tile0;
+    tile0 = blk * p.low + min(blk, p.tall);
+    return p.low + (blk < p.tall);
 }
 
 // TMA: rows of sign words are 16-byte aligned and come by TMA.
@@ -454,20 +455,22 @@ int ring_stages(const GroupedCall& c, Plan& p, int h) {
 cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
     Plan p{};
     for (int j = 0; j < 16; ++j) p.shift[j] = 1u << (15 - j);
-    p.tiles = (c.out + 15) / 16;
+    const int tiles = (c.out + 15) / 16;
     const int active = c.n < c.experts ? c.n : c.experts;  // experts expected to have slots, a pass of columns each
     // Block height: the rounds of blocks over the SMs times their length (a block's fixed cost is about one
     // tile), blocks as many as fill the rounds.
     double best = 0;
     for (int h = 1; h <= H && ring_stages(c, p, h) > 0; ++h) {
-        const long long least = (p.tiles + h - 1) / h, rounds = (active * least + sms - 1) / sms;
+        const long long least = (tiles + h - 1) / h, rounds = (active * least + sms - 1) / sms;
         long long nblk = rounds * sms / active;
-        nblk = nblk < least ? least : nblk > p.tiles ? p.tiles : nblk;
-        const double cost = (double)rounds * ((double)p.tiles / nblk + 1);
+        nblk = nblk < least ? least : nblk > tiles ? tiles : nblk;
+        const double cost = (double)rounds * ((double)tiles / nblk + 1);
         if (best == 0 || cost < best) best = cost, p.nblk = (int)nblk;
     }
-    const int h = (p.tiles + p.nblk - 1) / p.nblk;  // blocks have h or h - 1 tiles
+    const int h = (tiles + p.nblk - 1) / p.nblk;  // blocks have h or h - 1 tiles
     ring_stages(c, p, h);
+    p.low = tiles / p.nblk;
+    p.tall = tiles % p.nblk;
     return c.K % 128 == 0 ? launch_as<true>(c, p, h, status, st, sms) : launch_as<false>(c, p, h, status, st, sms);
 }
 
