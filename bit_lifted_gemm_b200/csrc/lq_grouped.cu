@@ -48,7 +48,7 @@ bool few_rows(const GroupedCall& c) { return slots_each(c) <= 8; }
 size_t grouped_workspace_size(const GroupedCall& c) {
     size_t need = decode_workspace(c);
     if (!need) need = slots_workspace(c);
-    if (!need && !few_rows(c) && c.offsets) need = grouped_tc_workspace_size(c.K, c.n);
+    if (!need && !few_rows(c)) need = grouped_tc_workspace_size(c, slots_each(c));
     return need > 256 ? need : 256;
 }
 

@@ -139,12 +139,27 @@ __device__ __forceinline__ void store_chunk(const GroupedCall& c, float (&z)[32]
     if (m < c.out) store_row<16, BF16>(c, gate, (long long)(slot0 + j0) * width + m / 2, width, count - j0);
 }
 
-// BN: slots of a full tile. VEC: K a multiple of 128, so that rows of sign words are
-// 16-byte aligned. GATHER: rows are given.
-template <int BN, bool VEC>
+// A layer's tiles cut along K, when they are too few or too uneven for the SMs (plan_split). A part's epilogue
+// warps write its sums to `part`; of a tile's parts, the warp that counts itself last adds them, in the order of
+// k whoever that is, and stores the outputs.
+struct Split {
+    int parts;
+    unsigned* count;  // [tiles][4 warps], cleared by the kernel before
+    float4* part;     // [tiles][parts][BN / 4][128], four slots each
+};
+
+__global__ void __launch_bounds__(256) clear_kernel(uint4* to, int n) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the products may start meanwhile
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < n) to[i] = make_uint4(0, 0, 0, 0);
+}
+
+// BN: slots of a full tile. SPLIT: tiles are cut along K. VEC: K a multiple of 128, so that rows of sign words are
+// 16-byte aligned.
+template <int BN, bool VEC, bool SPLIT>
 __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
     tc_kernel(const __grid_constant__ CUtensorMap tmap_u, const __grid_constant__ CUtensorMap tmap_all,
-              const __grid_constant__ GroupedCall c, unsigned* status) {
+              const __grid_constant__ GroupedCall c, const Split split, unsigned* status) {
     constexpr int STAGES = Ring<BN>::STAGES, SUB = Ring<BN>::SUB, A_STAGE = Ring<BN>::A_STAGE;
     constexpr int B_STAGE = Ring<BN>::B_STAGE, B_TILE = Ring<BN>::B_TILE, STEP = SUB * BK;
     constexpr int ISSUERS = Ring<BN>::ISSUERS, ACC = ISSUERS * BN;  // columns of a tile's accumulators
@@ -159,7 +174,7 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
     const uint32_t acc_full0 = empty0 + 8 * STAGES, acc_empty0 = acc_full0 + 16, drained = acc_empty0 + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kw = c.K >> 5, nkb = (c.K + STEP - 1) / STEP, nblk = (c.out + BM - 1) / BM;
+    const int kw = c.K >> 5, steps = (c.K + STEP - 1) / STEP, nblk = (c.out + BM - 1) / BM;
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < STAGES; ++st) {
@@ -196,6 +211,18 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
 
     UnitWalk walk;
     Unit u;
+    long long tile;              // the unit's tile, and its range of steps: [kb0, kb0 + nkb)
+    int part = 0, kb0 = 0, nkb = steps;
+    auto next = [&](long long unit) {
+        tile = unit;
+        if constexpr (SPLIT) {
+            tile = unit / split.parts;
+            part = (int)(unit - tile * split.parts);
+            kb0 = (int)((long long)part * steps / split.parts);
+            nkb = (int)((long long)(part + 1) * steps / split.parts) - kb0;
+        }
+        return walk.find<false>(c, BN, nblk, tile, lane, u);
+    };
     int st = 0, phase = 0;  // ring position, kept by each role
     auto advance = [&] {
         if (++st == STAGES) st = 0, phase ^= 1;
@@ -217,7 +244,7 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
     if (warp == 0) {
         // ---- u tiles
         int issued = 0;
-        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+        for (long long unit = blockIdx.x; go && next(unit); unit += gridDim.x) {
             const bool all = u.slots > BN - kBox;
             const int boxes = all ? BN / kBox : (u.slots + kBox - 1) / kBox;
             for (int kb = 0; kb < nkb; ++kb) {
@@ -230,10 +257,10 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
                     for (int x = 0; x < SUB; ++x) {
                         const uint32_t to = dst + x * B_TILE;
                         if (all)
-                            tma_load_2d(to, &tmap_all, kb * STEP + x * BK, u.slot0, bar);
+                            tma_load_2d(to, &tmap_all, (kb0 + kb) * STEP + x * BK, u.slot0, bar);
                         else
                             for (int i = 0; i < boxes; ++i)
-                                tma_load_2d(to + i * kBox * 128, &tmap_u, kb * STEP + x * BK, u.slot0 + i * kBox, bar);
+                                tma_load_2d(to + i * kBox * 128, &tmap_u, (kb0 + kb) * STEP + x * BK, u.slot0 + i * kBox, bar);
                     }
                 }
                 __syncwarp();
@@ -251,7 +278,7 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
         const int issuer = warp == 1 ? 0 : 1;
         int acc = 0, acc_phase = 0;
         const uint64_t a_desc = smem_desc_sw128(sA), b_desc = smem_desc_sw128(sB);
-        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+        for (long long unit = blockIdx.x; go && next(unit); unit += gridDim.x) {
             const uint32_t idesc = idesc_bf16_f32(BM, (u.slots + 15) / 16 * 16);
             if (!(go = wait(acc_empty0 + 8 * acc, acc_phase ^ 1))) break;
             tc_fence_after();
@@ -295,13 +322,13 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
         constexpr int WORDS = 2 * SUB, AHEAD = 16 / WORDS;  // sign words of a row and stage; stages loaded ahead
         const int group = (warp - UNPACK_WARP) >> 2, row = (threadIdx.x - 32 * UNPACK_WARP) & 127;
         const uint32_t row_off = (row >> 3) * 1024 + (row & 7) * 128, sw = row & 7;
-        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+        for (long long unit = blockIdx.x; go && next(unit); unit += gridDim.x) {
             const int r = min(u.blk * BM + row, c.out - 1);  // rows past `out` are computed but not stored
             // Past the row's end its last words are read again: u is zero there. (No branch: a load merged with
             // another value would be waited for at once.)
             const uint32_t* w0 = c.packed + ((long long)u.e * c.out + r) * kw;
             auto load = [&](int kb, uint32_t (&to)[WORDS]) {
-                const int x = WORDS * kb;
+                const int x = WORDS * (kb0 + kb);
                 if constexpr (VEC && SUB == 2) {
                     const uint4 v = __ldg(reinterpret_cast<const uint4*>(w0 + min(x, kw - 4)));
                     to[0] = v.x, to[1] = v.y, to[2] = v.z, to[WORDS - 1] = v.w;
@@ -318,10 +345,10 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
             uint32_t ahead[AHEAD][WORDS];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) load(begin + 2 * i, ahead[i]);
-            for (int kb0 = begin; kb0 < nkb && go; kb0 += 2 * AHEAD) {
+            for (int kb1 = begin; kb1 < nkb && go; kb1 += 2 * AHEAD) {
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    const int kb = kb0 + 2 * i;
+                    const int kb = kb1 + 2 * i;
                     if (kb >= nkb || !go) break;
                     uint32_t w[WORDS];
 #pragma unroll
@@ -354,8 +381,17 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
     } else {
         // ---- epilogue: a warp may only reach its own quarter of the TMEM lanes (warp % 4)
         const int q = warp & 3, width = c.glu ? c.out / 2 : c.out;
-        int acc = 0, acc_phase = 0, issuer0 = 0;  // issuer0: the issuer of the tile's first stage
-        for (long long unit = blockIdx.x; go && walk.find<false>(c, BN, nblk, unit, lane, u); unit += gridDim.x) {
+        int acc = 0, acc_phase = 0, issuer0 = 0;  // issuer0: the issuer of the unit's first stage
+        if constexpr (SPLIT) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are cleared
+        auto finish = [&](float (&z)[32], int c0, float sr, float br, int m) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, z[j], br);
+            if (c.o_bf16)
+                store_chunk<true>(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
+            else
+                store_chunk<false>(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
+        };
+        for (long long unit = blockIdx.x; go && next(unit); unit += gridDim.x) {
             const int m = u.blk * BM + q * 32 + lane;
             const long long at = (long long)u.e * c.out + min(m, c.out - 1);
             const float sr = __ldg(c.s + at), br = c.bias ? __ldg(c.bias + at) : 0.f;
@@ -376,15 +412,42 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j] += __uint_as_float(v[j]);
                 }
+                if constexpr (SPLIT) {
+                    float4* to = split.part + ((tile * split.parts + part) * BN + c0) / 4 * BM + q * 32 + lane;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) z[j] = fmaf(sr, z[j], br);
-                if (c.o_bf16)
-                    store_chunk<true>(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
-                else
-                    store_chunk<false>(c, z, m, width, u.slot0 + c0, u.slots - c0, lane);
+                    for (int j = 0; j < 32; j += 4)
+                        if (c0 + j < u.slots) __stcg(to + j / 4 * BM, make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]));
+                } else {
+                    finish(z, c0, sr, br, m);
+                }
             }
             tc_fence_before();
             mbar_arrive(acc_empty0 + 8 * acc);
+            if constexpr (SPLIT) {
+                __threadfence();  // the sums are there before the count says so
+                __syncwarp();
+                unsigned before = 0;
+                if (lane == 0) before = atomicAdd(split.count + tile * 4 + q, 1u);
+                if (__shfl_sync(0xffffffffu, before, 0) == split.parts - 1u) {
+                    __threadfence();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < u.slots; c0 += 32) {
+                        const float4* from = split.part + (tile * split.parts * BN + c0) / 4 * BM + q * 32 + lane;
+                        float z[32] = {};
+#pragma unroll 2
+                        for (int x = 0; x < split.parts; ++x, from += BN / 4 * BM) {
+                            float4 v[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                v[j] = c0 + 4 * j < u.slots ? __ldcg(from + j * BM) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                z[4 * j] += v[j].x, z[4 * j + 1] += v[j].y, z[4 * j + 2] += v[j].z, z[4 * j + 3] += v[j].w;
+                        }
+                        finish(z, c0, sr, br, m);
+                    }
+                }
+            }
             if (ISSUERS == 2) issuer0 ^= nkb & 1;
             if (++acc == 2) acc = 0, acc_phase ^= 1;
         }
@@ -431,8 +494,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ Gro
     }
 }
 
-template <int BN, bool VEC>
-cudaError_t launch_as(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
+template <int BN, bool VEC, bool SPLIT>
+cudaError_t launch_as(const GroupedCall& c, const Split& split, unsigned* status, cudaStream_t st, int sms) {
     EncodeTiledFn encode = encode_fn();
     if (!encode) return cudaErrorNotSupported;
     CUtensorMap map, map_all;  // u in boxes of kBox and of BN rows
@@ -450,23 +513,63 @@ cudaError_t launch_as(const GroupedCall& c, unsigned* status, cudaStream_t st, i
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(tc_kernel<BN, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(tc_kernel<BN, VEC, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)Ring<BN>::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    tc_kernel<BN, VEC><<<sms, Ring<BN>::THREADS, Ring<BN>::SMEM_BYTES, st>>>(map, map_all, c, status);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms);
+    cfg.blockDim = dim3(Ring<BN>::THREADS);
+    cfg.dynamicSmemBytes = Ring<BN>::SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = SPLIT ? 1 : 0;  // behind clear_kernel alone, which is launched when all before it is complete
+    return cudaLaunchKernelEx(&cfg, tc_kernel<BN, VEC, SPLIT>, map, map_all, c, split, status);
 }
 
 template <int BN>
-cudaError_t launch_bn(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms) {
-    return c.K % 128 == 0 ? launch_as<BN, true>(c, status, st, sms) : launch_as<BN, false>(c, status, st, sms);
+cudaError_t launch_bn(const GroupedCall& c, const Split& split, unsigned* status, cudaStream_t st, int sms) {
+    if (split.parts > 1)
+        return c.K % 128 == 0 ? launch_as<BN, true, true>(c, split, status, st, sms) : launch_as<BN, false, true>(c, split, status, st, sms);
+    return c.K % 128 == 0 ? launch_as<BN, true, false>(c, split, status, st, sms) : launch_as<BN, false, false>(c, split, status, st, sms);
 }
+
+int tile_slots(int each) { return each <= 64 ? 64 : each <= 128 ? 128 : 256; }
+
+// Parts along K of each tile of one layer: the rounds over the SMs times a part's steps and its own cost in steps
+// (its sums written and counted, all parts' read by the last, 4 to 20 us). us whole and in parts: 4096 x 10240 at 64 tokens 36
+// and 19.6 (4 parts), at 128 52 and 27, at 512 65 and 48; 11007 x 9728 at 61 tokens 37 and 44 (5 parts, not taken),
+// 13824 x 12288 at 256 71 and 101 (4 parts, not taken). Three rounds of parts bound the workspace.
+int plan_split(const GroupedCall& c, int bn, long long& tiles) {
+    constexpr int kSms = 148;
+    const int step = bn == 64 ? 128 : 64;
+    const double wide = bn == 64 ? 1 : bn == 128 ? 2 : 3.2;
+    const int steps = (c.K + step - 1) / step;
+    tiles = (long long)((c.out + BM - 1) / BM) * (((long long)c.n + bn - 1) / bn);
+    if (c.offsets || tiles >= 2 * kSms) return 1;
+    int best = 1;
+    double cost = 0.95 * ((tiles + kSms - 1) / kSms) * steps;
+    for (int parts = 2; parts <= 16 && parts <= steps && parts * tiles <= 3 * kSms; ++parts) {
+        const double with = (double)((tiles * parts + kSms - 1) / kSms) * ((steps + parts - 1) / parts + wide * (6 + 2.75 * parts));
+        if (with < cost) cost = with, best = parts;
+    }
+    return best;
+}
+
+size_t count_bytes(long long tiles) { return ((size_t)tiles * 16 + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t grouped_tc_workspace_size(int K, int n) { return (size_t)n * K * 2; }
+size_t grouped_tc_workspace_size(const GroupedCall& c, int each) {
+    if (c.offsets) return (size_t)c.n * c.K * 2;  // used when rows are given
+    long long tiles;
+    const int bn = tile_slots(each), parts = plan_split(c, bn, tiles);
+    return parts > 1 ? count_bytes(tiles) + (size_t)tiles * parts * bn * BM * 4 : 0;
+}
 
 cudaError_t launch_grouped_tc(const GroupedCall& call, void* ws, unsigned* status, cudaStream_t st, int sms, int each) {
     GroupedCall c = call;
@@ -478,9 +581,19 @@ cudaError_t launch_grouped_tc(const GroupedCall& call, void* ws, unsigned* statu
         c.tokens = c.n;
         c.rows = nullptr;
     }
-    if (each <= 64) return launch_bn<64>(c, status, st, sms);
-    if (each <= 128) return launch_bn<128>(c, status, st, sms);
-    return launch_bn<256>(c, status, st, sms);
+    const int bn = tile_slots(each);
+    long long tiles;
+    Split split{plan_split(c, bn, tiles), nullptr, nullptr};
+    if (split.parts > 1) {
+        split.count = static_cast<unsigned*>(ws);
+        split.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + count_bytes(tiles));
+        clear_kernel<<<(unsigned)((tiles + 255) / 256), 256, 0, st>>>(static_cast<uint4*>(ws), (int)tiles);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (bn == 64) return launch_bn<64>(c, split, status, st, sms);
+    if (bn == 128) return launch_bn<128>(c, split, status, st, sms);
+    return launch_bn<256>(c, split, status, st, sms);
 }
 
 }  // namespace lq

@@ -140,7 +140,7 @@ cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cud
 // Its kernel for few rows per expert (lq_grouped_mma.cu), on `sms` CTAs.
 cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms);
 // Its kernel for many rows per expert (lq_grouped_tc.cu): bf16 u, about `each` slots to an expert.
-size_t grouped_tc_workspace_size(int K, int n);  // used when rows are given
+size_t grouped_tc_workspace_size(const GroupedCall& c, int each);  // sizes of c, and whether it has offsets
 cudaError_t launch_grouped_tc(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st, int sms, int each);
 
 // Its path for a few slots, a slot at a time: the decode GEMV with the epilogue on u made fp32, a share of the

@@ -269,6 +269,63 @@ def test_grouped_nothing_routed(lq):
     assert bool((out_t == 2.0).all())
 
 
+@pytest.mark.parametrize("out,K,tokens", [(130, 12288, 9), (1001, 8224, 64), (640, 10240, 100), (257, 16384, 130), (258, 20480, 300),
+                                          (4096, 10240, 33), (2050, 20512, 512)])
+def test_layers_cut_along_k(lq, out, K, tokens):
+    """Few tiles and a long K: the parts of a tile are added in order, whatever the workspace held; values, gates, exact
+    integers, and infinities that meet from different parts."""
+    import torch
+    rng = np.random.default_rng([25, out, K, tokens])
+    need = lq.gemm_epilogue_workspace_size(out, K, tokens)
+    assert need > 256
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    for act, glu, o_t in (("gelu", False, "f32"), ("silu", out % 2 == 0, "bf16")):
+        got, want, tol = run_layer(lq, rng, out, K, tokens, "bf16", o_t, act, glu, True, True, workspace=ws)
+        plain.assert_close(f64(got), want, tol, o_t == "bf16")
+    packed, _ = make_layer(rng, (), out, K)
+    weights = dev(packed), gpu(np.ones(out))
+    u = rng.integers(-8, 9, (tokens, K)).astype(np.float32)
+    got = lq.gemm_epilogue(*weights, gpu(u, True), workspace=ws)
+    assert np.array_equal(f64(got), u.astype(np.float64) @ plain.signs(packed).T)
+    x = gpu(rng.standard_normal((tokens, K)), True)
+    first = lq.gemm_epilogue(*weights, x, workspace=ws)
+    for _ in range(20):
+        assert torch.equal(lq.gemm_epilogue(*weights, x, workspace=ws), first)
+    u[1, 5], u[1, K - 3] = np.inf, -np.inf
+    got = f64(lq.gemm_epilogue(*weights, gpu(u, True), workspace=ws))[1]
+    sg = plain.signs(packed)
+    opposed = sg[:, 5] == sg[:, K - 3]
+    assert np.isnan(got[opposed]).all() and np.array_equal(got[~opposed], np.where(sg[~opposed, 5] > 0, np.inf, -np.inf))
+
+
+def test_layers_cut_along_k_in_graphs_and_streams(lq):
+    import torch
+    rng = np.random.default_rng(26)
+    out, K, tokens = 384, 12288, 64
+    packed, s = make_layer(rng, (), out, K)
+    weights = dev(packed), gpu(s)
+    inputs = [gpu(rng.standard_normal((tokens, K)), True) for _ in range(2)]
+    alone = [lq.gemm_epilogue(*weights, u) for u in inputs]
+    spaces = [torch.empty(lq.gemm_epilogue_workspace_size(out, K, tokens), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.empty_like(a) for a in alone]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            for _ in range(3):
+                lq.gemm_epilogue(*weights, inputs[i], out=outs[i], workspace=spaces[i])
+        graphs.append(g)
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], alone[i])
+
+
 def test_grouped_calls_without_slots_leave_the_next_call_alone(lq):
     """On one workspace: what calls without any slot prepare there must not come after what a call with slots does."""
     import torch
