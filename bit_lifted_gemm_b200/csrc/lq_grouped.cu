@@ -23,8 +23,9 @@ int slots_each(const GroupedCall& c) {
 
 // Tokens of one layer that take the decode GEMV on u made fp32 (1.5 us), unless its plan does not fit: one or two,
 // and nine to sixteen where the tcgen05 kernel's 128-row tiles exceed the 148 SMs. Measured in us, this path
-// against the kernel that would take them else: 13824 x 12288 at 1 / 2 / 16 tokens 12.4 / 14.4 / 42 against
-// 17.7 / 18.9 / 37, 28672 x 20480 26.4 / 36.4 / 83 against 58 / 59 / 130, 4096 x 10240 8.7 / 10.5 / 34 against 10.6 / 10.8 / 31.
+// against the kernel that would take them else: 13824 x 12288 at 1 / 2 / 16 tokens 12.8 / 14.6 / 42 against
+// 18.7 / 18.3 / 37 to 43, 28672 x 20480 26.3 / 36.4 / 82 against 52 / 52 / 134, 4096 x 10240 8.7 / 10.6 / 34 against
+// 9.7 / 10.1 / 17.
 size_t decode_workspace(const GroupedCall& c) {
     if (c.experts != 1 || c.offsets || c.n > 16 || (c.n > 2 && (c.n <= 8 || c.out <= 148 * 128))) return 0;
     return gemv_epilogue_bf16_workspace_size(c.out, c.K, c.n);
@@ -32,15 +33,15 @@ size_t decode_workspace(const GroupedCall& c) {
 
 // Slots of experts that take the same GEMV one by one, a share of the SMs each: up to two an expert, if the shares
 // suffice and rows of words are 16-byte aligned. us against the mma.sync kernel: 2 slots of 8 experts of 11008 x 10240
-// 15 against 27, 16 slots of 16 of 4096 x 10240 29 against 47, 128 of 128 99 against 163; four slots an expert, 16 of 4
-// experts, 28 against 20.
+// 15 against 27, of 4096 x 10240 one slot to each of 16 experts 30 against 62, of 128 188 against 393, two to each of
+// 8 29 against 34; four to each of 4 28 against 20.
 size_t slots_workspace(const GroupedCall& c) {
     if (!c.offsets || slots_each(c) > 2 || c.n > 148 || c.K % 128 != 0) return 0;
     return gemv_slots_workspace_size(c.out, c.K, c.n);
 }
 
 // Up to eight slots an expert, one pass of the mma.sync kernel, which reads the weights once for all of them (us at 8
-// and 9 to 16 tokens of 13824 x 12288: 20 and, in two passes, 38; the tcgen05 kernel 37 for either).
+// and 9 to 16 tokens of 13824 x 12288: 20 and, in two passes, 38; the tcgen05 kernel 37 to 43 for either).
 bool few_rows(const GroupedCall& c) { return slots_each(c) <= 8; }
 
 }  // namespace

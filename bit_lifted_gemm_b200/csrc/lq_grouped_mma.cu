@@ -23,8 +23,8 @@
 //
 // What bounds it: the expansion. An MMA takes eight clocks of the tensor pipe of a scheduler, the four
 // shifts and four logic operations of its signs eight of the half-rate integer and logic pipes each,
-// and ~17 clocks are measured: 20 us for 8 tokens of 13824 x 12288 (1.06 TB/s of signs), 62 us for 8 gated tokens of
-// 28672 x 20480. Four groups of consumers on blocks of four tiles took 26 and 77 us.
+// and ~20 clocks are measured: 20 us for 8 tokens of 13824 x 12288 (1.06 TB/s of signs), 54 us for 8 gated tokens of
+// 28672 x 20480 (1.36 TB/s).
 //
 // Order of k. Thread (g, t) = (lane / 4, lane % 4) owns words t and 4 + t of the
 // warp's eight. Register j of a word holds bits j and j + 16 at the sign positions

@@ -17,7 +17,8 @@
 // With `rows`, a kernel before it copies the slots' rows of u into the workspace: gathering
 // them in this kernel, four to a TMA instruction, took 1200 clocks per 64 k of 256 slots
 // (the MMAs take 512), and with cp.async 1900; the copy costs n K bytes written and read.
-// Products are exact; only the fp32 sums round. Every wait is bounded.
+// Few tiles of a single layer are cut along K, so that they fill the SMs (plan_split). Products are exact; only the
+// fp32 sums round. Every wait is bounded.
 //
 // What bounds it. Wide tiles: the tensor cores under the power cap (13824 x 12288, 2048 tokens, gated:
 // 427 us = 1630 TFLOP/s in short bursts, 499 us = 1394 of the 1434 TFLOP/s that the library's product
