@@ -618,3 +618,42 @@ def test_wrong_tensors_are_refused(lq):
         lq._check(rc, "lq_combine_rows")
     with pytest.raises(lq.LQError):  # workspace too small
         lq.gemv_epilogue(pk[0], sd[0], u.float(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_two_threads_at_once(lq):
+    """Calls of two host threads, each on a stream and workspaces of its own, give what they give alone."""
+    import threading
+
+    import torch
+    rng = np.random.default_rng(27)
+    work = []
+    for out, K, tokens in ((300, 12288, 1), (514, 4096, 6), (384, 12288, 64), (1000, 1536, 300)):
+        packed, s = make_layer(rng, (), out, K)
+        work.append((dev(packed), gpu(s), gpu(rng.standard_normal((tokens, K)), True)))
+    ids = ints(rng.integers(0, 40, (3000, 8)))
+
+    def calls():
+        return [lq.gemm_epilogue(*w, act="gelu") for w in work] + [lq.gemv_epilogue(*w[:2], w[2].float()) for w in work[:2]] + [
+            t for t in lq.group_rows(ids, 40)]
+
+    alone = calls()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = calls()
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, alone)):
+                        wrong.append("results differ")
+        except Exception as e:  # a thread's exception would be lost
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=run) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
