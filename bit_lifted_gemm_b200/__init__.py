@@ -374,22 +374,34 @@ def _activation(act):
     return ACTIVATIONS[act]
 
 
+_INT_MAX = 2 ** 31 - 1  # the C ABI's counts are ints, and ctypes drops the bits above without a word
+
+
+def _counts(where, *counts):
+    if max(counts) > _INT_MAX:
+        raise LQError(LQ_ERR_INVALID_ARG, where)
+
+
+def _fit(*counts):
+    return -_INT_MAX <= min(counts) and max(counts) <= _INT_MAX
+
+
 @functools.lru_cache(maxsize=1024)
 def gemm_epilogue_workspace_size(out_rows: int, K: int, tokens: int) -> int:
     """Bytes of workspace gemm_epilogue needs (0: refused sizes)."""
-    return int(lib.lq_gemm_epilogue_workspace_size(out_rows, K, tokens))
+    return 0 if not _fit(out_rows, K, tokens) else int(lib.lq_gemm_epilogue_workspace_size(out_rows, K, tokens))
 
 
 @functools.lru_cache(maxsize=1024)
 def gemv_epilogue_workspace_size(out_rows: int, K: int, batch: int) -> int:
     """Bytes of workspace gemv_epilogue needs (0: refused sizes)."""
-    return int(lib.lq_gemv_epilogue_workspace_size(out_rows, K, batch))
+    return 0 if not _fit(out_rows, K, batch) else int(lib.lq_gemv_epilogue_workspace_size(out_rows, K, batch))
 
 
 @functools.lru_cache(maxsize=1024)
 def gemm_grouped_workspace_size(experts: int, out_rows: int, K: int, n: int) -> int:
     """Bytes of workspace gemm_grouped needs (0: refused sizes)."""
-    return int(lib.lq_gemm_grouped_workspace_size(experts, out_rows, K, n))
+    return 0 if not _fit(experts, out_rows, K, n) else int(lib.lq_gemm_grouped_workspace_size(experts, out_rows, K, n))
 
 
 def _scratch(ws, need, like):
@@ -405,14 +417,16 @@ def _scratch(ws, need, like):
 
 def _layer_epilogue(fn, size_fn, u_type, packed, s, u, bias, act, glu, residual, o_dtype, out, workspace, stream):
     import torch
+    if u.dim() != 2 or packed.dim() != 2:
+        raise ValueError("packed must be [out][K/32] and u [tokens][K]")
+    tokens, K = u.shape
+    rows = packed.shape[0]
+    _counts(fn, tokens, K, rows)
     if _elsewhere(u, stream, "u"):
         with _on(u, stream):
             return _layer_epilogue(fn, size_fn, u_type, packed, s, u, bias, act, glu, residual, o_dtype, out, workspace,
                                    None)
-    if u.dim() != 2 or packed.dim() != 2:
-        raise ValueError("packed must be [out][K/32] and u [tokens][K]")
-    tokens, K = u.shape
-    rows, dev = packed.shape[0], u.get_device()
+    dev = u.get_device()
     ot, o_t = _float_type(o_dtype if out is None else out.dtype)
     width = rows // 2 if glu else rows
     out, o = _result(out, "out", ot, (tokens, width), u)
@@ -458,14 +472,16 @@ def gemm_grouped(packed, s, u, offsets, n, rows=None, bias=None, act=None, glu=F
     [experts][out]). offsets and rows, as group_rows gives them, stay on the device.
     Slots of no expert are not written: uninitialized when `out` is allocated here."""
     import torch
-    if _elsewhere(u, stream, "u"):
-        with _on(u, stream):
-            return gemm_grouped(packed, s, u, offsets, n, rows, bias, act, glu, o_dtype, out, workspace)
     if u.dim() != 2 or packed.dim() != 3:
         raise ValueError("packed must be [experts][out][K/32] and u [tokens][K]")
     tokens, K = u.shape
     experts, out_rows = packed.shape[:2]
-    n, dev = int(n), u.get_device()
+    n = int(n)
+    _counts("lq_gemm_grouped", n, tokens, K, experts, out_rows)
+    if _elsewhere(u, stream, "u"):
+        with _on(u, stream):
+            return gemm_grouped(packed, s, u, offsets, n, rows, bias, act, glu, o_dtype, out, workspace)
+    dev = u.get_device()
     ot, o_t = _float_type(o_dtype if out is None else out.dtype)
     width = out_rows // 2 if glu else out_rows
     out, o = _result(out, "out", ot, (n, width), u)
@@ -486,12 +502,13 @@ def group_rows(expert_ids, experts, offsets=None, rows=None, slots=None, stream=
     order, rows the token of each slot (-1 past the last), slots the slot of each choice (-1 for
     ids outside 0..experts-1)."""
     import torch
-    if _elsewhere(expert_ids, stream, "expert_ids"):
-        with _on(expert_ids, stream):
-            return group_rows(expert_ids, experts, offsets, rows, slots)
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be [tokens][topk]")
     tokens, topk = expert_ids.shape
+    _counts("lq_group_rows", tokens, topk, experts)
+    if _elsewhere(expert_ids, stream, "expert_ids"):
+        with _on(expert_ids, stream):
+            return group_rows(expert_ids, experts, offsets, rows, slots)
     dev, i32 = expert_ids.get_device(), torch.int32
     offsets, offsets_at = _result(offsets, "offsets", i32, (experts + 1,), expert_ids)
     rows, rows_at = _result(rows, "rows", i32, (tokens * topk,), expert_ids)
@@ -506,13 +523,14 @@ def combine_rows(y, slots, weights, residual=None, out=None, stream=None):
     int32 [tokens][topk] (values outside 0..n-1 add nothing), weights fp32 [tokens][topk], residual and o
     [tokens][width] in y's type."""
     import torch
-    if _elsewhere(y, stream, "y"):
-        with _on(y, stream):
-            return combine_rows(y, slots, weights, residual, out)
     if y.dim() != 2 or slots.dim() != 2:
         raise ValueError("y must be [n][width] and slots [tokens][topk]")
     n, width = y.shape
     tokens, topk = slots.shape
+    _counts("lq_combine_rows", n, width, tokens, topk)
+    if _elsewhere(y, stream, "y"):
+        with _on(y, stream):
+            return combine_rows(y, slots, weights, residual, out)
     dev = y.get_device()
     yt, y_t = _float_type(y.dtype, "y's type")
     out, o = _result(out, "out", yt, (tokens, width), y)

@@ -160,3 +160,41 @@ def test_experts_block_checks_its_widths():
             block.step(*bad)
     with pytest.raises(ValueError):  # model = 40 channels lift to 96 columns = 3 words, hidden = 8 is no multiple of d
         ExpertMLP(both, s, torch.zeros((2, 40, 1), dtype=torch.int32), s, M)
+
+
+OVER = 2 ** 32 + 8  # as a C int this is 8, a count that the library takes
+
+
+@pytest.mark.parametrize("which", ["gemm out", "gemm tokens", "gemv out", "grouped n", "grouped out", "ids", "experts", "y", "width", "slots"])
+def test_counts_past_32_bits_are_refused(which):
+    """The binding's own check, before it asks for a device: tensors without storage stand for the large ones."""
+    import torch
+
+    import bit_lifted_gemm_b200 as lq
+
+    def t(shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    i32, bf = torch.int32, torch.bfloat16
+    call = {
+        "gemm out": lambda: lq.gemm_epilogue(t((OVER, 1), i32), t((OVER,)), t((1, 32), bf)),
+        "gemm tokens": lambda: lq.gemm_epilogue(t((4, 1), i32), t((4,)), t((OVER, 32), bf)),
+        "gemv out": lambda: lq.gemv_epilogue(t((OVER, 1), i32), t((OVER,)), t((1, 32))),
+        "grouped n": lambda: lq.gemm_grouped(t((2, 1, 1), i32), t((2, 1)), t((8, 32), bf), t((3,), i32), OVER),
+        "grouped out": lambda: lq.gemm_grouped(t((2, OVER, 1), i32), t((2, OVER)), t((8, 32), bf), t((3,), i32), 8),
+        "ids": lambda: lq.group_rows(t((OVER, 1), i32), 4),
+        "experts": lambda: lq.group_rows(t((4, 2), i32), OVER),
+        "y": lambda: lq.combine_rows(t((OVER, 1)), t((4, 2), i32), t((4, 2))),
+        "width": lambda: lq.combine_rows(t((1, OVER)), t((4, 2), i32), t((4, 2))),
+        "slots": lambda: lq.combine_rows(t((4, 1)), t((OVER, 1), i32), t((OVER, 1))),
+    }[which]
+    with pytest.raises(lq.LQError, match="LQ_ERR_INVALID_ARG"):
+        call()
+
+
+def test_workspace_sizes_of_counts_past_32_bits():
+    import bit_lifted_gemm_b200 as lq
+    for over in (OVER, -OVER):
+        assert lq.gemm_epilogue_workspace_size(over, 64, 4) == lq.gemm_epilogue_workspace_size(8, 64, over) == 0
+        assert lq.gemv_epilogue_workspace_size(over, 64, 4) == lq.gemv_epilogue_workspace_size(8, 64 + 2 * over, 4) == 0
+        assert lq.gemm_grouped_workspace_size(2, over, 64, 4) == lq.gemm_grouped_workspace_size(2, 8, 64, over) == 0
