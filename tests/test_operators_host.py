@@ -198,3 +198,29 @@ def test_workspace_sizes_of_counts_past_32_bits():
         assert lq.gemm_epilogue_workspace_size(over, 64, 4) == lq.gemm_epilogue_workspace_size(8, 64, over) == 0
         assert lq.gemv_epilogue_workspace_size(over, 64, 4) == lq.gemv_epilogue_workspace_size(8, 64 + 2 * over, 4) == 0
         assert lq.gemm_grouped_workspace_size(2, over, 64, 4) == lq.gemm_grouped_workspace_size(2, 8, 64, over) == 0
+
+
+def test_experts_block_checks_what_the_lift_reads():
+    """M and the whitening blocks go to kernels that take their extents from the other tensors' shapes."""
+    import torch
+
+    from bit_lifted_gemm_b200.experts import ExpertMLP
+    i32 = torch.int32
+    layers = (torch.zeros((2, 40, 2), dtype=i32), torch.zeros((2, 40)), torch.zeros((2, 40, 2), dtype=i32), torch.zeros((2, 40)))
+    M = torch.zeros((20, 24))  # model = 40 and hidden = 20 channels lift to 48 and 24 columns: 64 and 32
+    layers = (layers[0], layers[1], layers[2][:, :, :1].contiguous(), layers[3])
+    block = ExpertMLP(*layers, M, tinv_in=torch.zeros((5, 8, 8)), tinv_hidden=torch.zeros((5, 4, 4)))
+    for bad in (M.double(), M.t().contiguous().t(), M[0]):
+        with pytest.raises(ValueError):
+            ExpertMLP(*layers, bad)
+    z = torch.zeros
+    for model, hidden in (((5, 4, 4), (5, 8, 8)), ((4, 8, 8), None), (None, (4, 4, 4)), ((40, 40), None), ((5, 8, 4), None),
+                          ((1, 0, 0), None), ((3, 16, 16), None)):
+        with pytest.raises(ValueError, match="tinv"):
+            ExpertMLP(*layers, M, tinv_in=None if model is None else z(model), tinv_hidden=None if hidden is None else z(hidden))
+    for bad in (z((5, 8, 8), dtype=torch.float64), z((5, 8, 8)).transpose(1, 2), z((5, 8, 8), device="meta")):
+        with pytest.raises(ValueError, match="tinv"):
+            ExpertMLP(*layers, M, tinv_in=bad)
+    x, ids, w = z((5, 40), dtype=torch.bfloat16, device="meta"), z((5, 2), dtype=i32), z((5, 2))
+    with pytest.raises(ValueError, match="device"):
+        block.step(x, ids, w)
