@@ -614,7 +614,8 @@ int lq_get_device_status(void* stream) {
     const unsigned bounds = lq::debug_take_gemm() | lq::debug_take_lift() | lq::debug_take_lift_kron() |
                             lq::debug_take_lift_tc() | lq::debug_take_lift_kron_tc() | lq::debug_take_encode() |
                             lq::debug_take_pack() | lq::debug_take_rows() | lq::debug_take_grouped_mma() |
-                            lq::debug_take_grouped_tc() | lq::debug_take_selftest();
+                            lq::debug_take_grouped_tc() | lq::debug_take_gemv() | lq::debug_take_gemv_tc() |
+                            lq::debug_take_selftest();
     if (bounds) return LQ_ERR_BOUNDS;
 #endif
     return (v & LQ_DEV_TIMEOUT) ? LQ_ERR_TIMEOUT : LQ_OK;

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "lq.h"
+#include "lq_debug.cuh"
 #include "lq_decode.h"
 
 namespace lq {
@@ -80,9 +81,12 @@ __device__ __forceinline__ void store_elem(void* p, long long i, bool bf16, floa
 
 // The decode kernels' epilogue of weight row r of `count` columns from column 0 on, z with the scale applied and
 // no bias yet. Called by the lanes of rows 2i and 2i + 1 together, which are neighbours, when gated. The
-// choices are made outside the loops over the columns.
+// choices are made outside the loops over the columns. `columns`: rows of o and of the residual, for the debug build.
 template <int N>
-__device__ __forceinline__ void finish_row(const DecodeEpilogue& e, int out, int c0, int count, int r, float (&z)[N], int lane) {
+__device__ __forceinline__ void finish_row(const DecodeEpilogue& e, int out, int columns, int c0, int count, int r, float (&z)[N],
+                                           int lane) {
+    const long long extent = (long long)columns * (e.glu ? out / 2 : out);
+    (void)extent;
     const float bias = e.bias ? __ldg(e.bias + r) : 0.f;
 #pragma unroll
     for (int c = 0; c < N; ++c) z[c] += bias;
@@ -103,13 +107,13 @@ __device__ __forceinline__ void finish_row(const DecodeEpilogue& e, int out, int
     if (e.residual) {
         float res[N];
 #pragma unroll
-        for (int c = 0; c < N; ++c) res[c] = c < count ? load_elem(e.residual, at + c * step, e.o_bf16) : 0.f;
+        for (int c = 0; c < N; ++c) res[c] = c < count && LQ_IN_BOUNDS(at + c * step, extent) ? load_elem(e.residual, at + c * step, e.o_bf16) : 0.f;
 #pragma unroll
         for (int c = 0; c < N; ++c) z[c] += res[c];
     }
 #pragma unroll
     for (int c = 0; c < N; ++c)
-        if (c < count) store_elem(e.o, at + c * step, e.o_bf16, z[c]);
+        if (c < count && LQ_IN_BOUNDS(at + c * step, extent)) store_elem(e.o, at + c * step, e.o_bf16, z[c]);
 }
 
 }  // namespace lq

@@ -705,7 +705,7 @@ __global__ void __maxnreg__(128)  // 384 threads: leaves registers for a lift be
                 float z[1] = {res};
                 DecodeEpilogue epi = p.epi;
                 if (epi.bias) epi.bias += wrow;
-                finish_row(epi, p.out, c0 + c, 1, m, z, lane);
+                finish_row(epi, p.out, p.per ? p.nslots : p.c0 + p.ncols, c0 + c, 1, m, z, lane);
             } else {
                 *part = res;
             }
@@ -1017,11 +1017,13 @@ __global__ void __launch_bounds__(256)
     if (x >= chunks) return;
     const int row = rows ? __ldg(rows + i) : i;
     const uint4 zero = {0, 0, 0, 0};
-    const uint4 v = row >= 0 && row < tokens ? __ldg(u + (long long)row * chunks + x) : zero;
+    const bool there = row >= 0 && row < tokens && LQ_IN_BOUNDS((long long)row * chunks + x, (long long)tokens * chunks);
+    const uint4 v = there ? __ldg(u + (long long)row * chunks + x) : zero;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[2 * j] = __uint_as_float(w[j] << 16), f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    if (!LQ_IN_BOUNDS((long long)i * chunks + x, (long long)gridDim.y * chunks)) return;
     to += 2 * ((long long)i * chunks + x);
     to[0] = make_float4(f[0], f[1], f[2], f[3]);
     to[1] = make_float4(f[4], f[5], f[6], f[7]);
@@ -1089,3 +1091,5 @@ cudaError_t launch_lift_gemv(const void* a, bool a_bf16, int batch, int in, cons
 }
 
 }  // namespace lq
+
+LQ_DEBUG_FLAG_TAKE(debug_take_gemv)

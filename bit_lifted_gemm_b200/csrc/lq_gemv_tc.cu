@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(tc_threads(MT), 1)
                     else
                         p.o[(size_t)c * p.out + r] = res;
                 }
-                if constexpr (EPI) finish_row(p.epi, p.out, 0, p.batch, (int)r, z, lane);
+                if constexpr (EPI) finish_row(p.epi, p.out, p.batch, 0, p.batch, (int)r, z, lane);
             };
             // ---- drain tile by tile: sum the planes of each column (plane p =
             // columns p * bpad ..), then store the result (the group is this
@@ -860,3 +860,5 @@ cudaError_t launch_gemv_tc(const uint32_t* packed, const float* s, const DecodeP
 }
 
 }  // namespace lq
+
+LQ_DEBUG_FLAG_TAKE(debug_take_gemv_tc)

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int m = 0; m < MANY; ++m) {
                     const int slot = slot0 + m * per;
                     const bool there = slot < u.slots;
-                    res[m] = there && c.residual ? load_elem(c.residual, at0 + m * at_step, c.o_bf16) : 0.f;
+                    res[m] = there && c.residual && LQ_IN_BOUNDS(at0 + m * at_step, (long long)c.n * width) ? load_elem(c.residual, at0 + m * at_step, c.o_bf16) : 0.f;
                     float z[2] = {0.f, 0.f};
                     const float* sums = red + (there ? slot : slot0) * p.rp + r;
                     if (c.glu) {

@@ -98,7 +98,7 @@ __device__ __forceinline__ void store_row(const GroupedCall& c, float (&y)[N], l
         const T* res = static_cast<const T*>(c.residual) + at;
         T r[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) r[j] = j < count ? __ldg(res + (long long)j * width) : T(0);
+        for (int j = 0; j < N; ++j) r[j] = j < count && LQ_IN_BOUNDS(at + (long long)j * width, extent) ? __ldg(res + (long long)j * width) : T(0);
 #pragma unroll
         for (int j = 0; j < N; ++j) y[j] += Elem<BF16>::to_float(r[j]);
     }
@@ -328,17 +328,23 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
             // Past the row's end its last words are read again: u is zero there. (No branch: a load merged with
             // another value would be waited for at once.)
             const uint32_t* w0 = c.packed + ((long long)u.e * c.out + r) * kw;
+            auto words_there = [&](int x, int count) {  // `count` words from word x of the row
+                return LQ_IN_BOUNDS(w0 - c.packed + x, (long long)c.experts * c.out * kw - count + 1);
+            };
             auto load = [&](int kb, uint32_t (&to)[WORDS]) {
                 const int x = WORDS * (kb0 + kb);
                 if constexpr (VEC && SUB == 2) {
+                    if (!words_there(min(x, kw - 4), 4)) return;
                     const uint4 v = __ldg(reinterpret_cast<const uint4*>(w0 + min(x, kw - 4)));
                     to[0] = v.x, to[1] = v.y, to[2] = v.z, to[WORDS - 1] = v.w;
                 } else if constexpr (VEC) {
+                    if (!words_there(min(x, kw - 2), 2)) return;
                     const uint2 v = __ldg(reinterpret_cast<const uint2*>(w0 + min(x, kw - 2)));
                     to[0] = v.x, to[1] = v.y;
                 } else {
 #pragma unroll
-                    for (int i = 0; i < WORDS; ++i) to[i] = __ldg(w0 + min(x + i, kw - 1));
+                    for (int i = 0; i < WORDS; ++i)
+                        if (words_there(min(x + i, kw - 1), 1)) to[i] = __ldg(w0 + min(x + i, kw - 1));
                 }
             };
             const int st0 = st, phase0 = phase;  // ring position of the unit's first stage
@@ -383,6 +389,8 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
         // ---- epilogue: a warp may only reach its own quarter of the TMEM lanes (warp % 4)
         const int q = warp & 3, width = c.glu ? c.out / 2 : c.out;
         int acc = 0, acc_phase = 0, issuer0 = 0;  // issuer0: the issuer of the unit's first stage
+        const long long tiles = (long long)nblk * ((c.n + BN - 1) / BN), parts_extent = tiles * split.parts * (BN / 4) * BM;
+        (void)parts_extent;
         if constexpr (SPLIT) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are cleared
         auto finish = [&](float (&z)[32], int c0, float sr, float br, int m) {
 #pragma unroll
@@ -417,7 +425,8 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
                     float4* to = split.part + ((tile * split.parts + part) * BN + c0) / 4 * BM + q * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        if (c0 + j < u.slots) __stcg(to + j / 4 * BM, make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]));
+                        if (c0 + j < u.slots && LQ_IN_BOUNDS(to + j / 4 * BM - split.part, parts_extent))
+                            __stcg(to + j / 4 * BM, make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]));
                 } else {
                     finish(z, c0, sr, br, m);
                 }
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
                 __threadfence();  // the sums are there before the count says so
                 __syncwarp();
                 unsigned before = 0;
-                if (lane == 0) before = atomicAdd(split.count + tile * 4 + q, 1u);
+                if (lane == 0 && LQ_IN_BOUNDS(tile, tiles)) before = atomicAdd(split.count + tile * 4 + q, 1u);
                 if (__shfl_sync(0xffffffffu, before, 0) == split.parts - 1u) {
                     __threadfence();
 #pragma unroll 1
@@ -440,7 +449,9 @@ __global__ void __launch_bounds__(Ring<BN>::THREADS, 1)
                             float4 v[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                v[j] = c0 + 4 * j < u.slots ? __ldcg(from + j * BM) : make_float4(0.f, 0.f, 0.f, 0.f);
+                                v[j] = c0 + 4 * j < u.slots && LQ_IN_BOUNDS(from + j * BM - split.part, parts_extent)
+                                           ? __ldcg(from + j * BM)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 z[4 * j] += v[j].x, z[4 * j + 1] += v[j].y, z[4 * j + 2] += v[j].z, z[4 * j + 3] += v[j].w;

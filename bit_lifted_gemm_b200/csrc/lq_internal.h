@@ -59,6 +59,8 @@ cudaError_t launch_selftest_bounds(cudaStream_t st);
 // Debug build: read and clear the bounds flag of each source file (non-zero after
 // a failed check), on the current device.
 unsigned debug_take_gemm();
+unsigned debug_take_gemv();
+unsigned debug_take_gemv_tc();
 unsigned debug_take_lift();
 unsigned debug_take_lift_kron();
 unsigned debug_take_lift_tc();

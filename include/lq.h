@@ -30,10 +30,12 @@
  *  - Debug build: liblq_debug.so, the same entry points compiled with
  *    -DLQ_DEBUG. Its kernels test the element index of each computed global
  *    load and store of the pack, lift, Kronecker lift, prefill GEMM and
- *    encoder kernels, and of the row operators, the copies of rows and the
- *    stores of the grouped products, against the extent of its buffer (from the call's
- *    arguments) before the access; a failed test skips the access and latches
- *    LQ_ERR_BOUNDS. Nothing traps. TMA copies are bounded by their tensor maps
+ *    encoder kernels and of the row operators, and in the fused-epilogue and
+ *    grouped products the copies of rows of u, the loads of signs and u by address,
+ *    the partial sums of a cut along K, the loads of the residual and the stores of o,
+ *    against the extent of its buffer (from the call's arguments) before the access
+ *    (the decode GEMVs' own loads, and those of s and bias, carry no test); a
+ *    failed test skips the access and latches LQ_ERR_BOUNDS. Nothing traps. TMA copies are bounded by their tensor maps
  *    in both builds. The release library compiles the tests away.
  *  - Packed signs: 32 per uint32, least significant bit first along the
  *    lifted axis, bit 1 = +1, row-major [out][K/32].

@@ -224,3 +224,42 @@ def test_experts_block_checks_what_the_lift_reads():
     x, ids, w = z((5, 40), dtype=torch.bfloat16, device="meta"), z((5, 2), dtype=i32), z((5, 2))
     with pytest.raises(ValueError, match="device"):
         block.step(x, ids, w)
+
+
+def _body(text, name):
+    """The braces after the first definition of a function of this name."""
+    import re
+    start = next(m.end() for m in re.finditer(rf"\b{name}\s*\(", text)
+                 if re.match(r"[^;{]*\)\s*\{", text[m.end():], re.S))
+    at = text.index("{", start)
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at: i + 1]
+
+
+def test_debug_build_checks_the_operators_kernels():
+    """What the header says the debug build checks of these operators is checked, and every flag is read."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_lifted_gemm_b200", "csrc")
+
+    def read(f):
+        with open(os.path.join(csrc, f)) as h:
+            return h.read()
+
+    for f, functions in (("lq_epilogue.cuh", ["finish_row"]), ("lq_gemv.cu", ["widen_kernel"]), ("lq_grouped_mma.cu", ["mma_kernel"]),
+                         ("lq_grouped_tc.cu", ["store_row", "gather_kernel", "tc_kernel"]),
+                         ("lq_rows.cu", ["group_kernel", "combine_kernel"])):
+        for name in functions:
+            assert "LQ_IN_BOUNDS" in _body(read(f), name), (f, name)
+    flags = set()
+    for f in sorted(os.listdir(csrc)):
+        text = read(f)
+        if f.endswith(".cu"):
+            shared = [h for h in re.findall(r'#include "(\w+\.cuh)"', text) if h != "lq_debug.cuh" and "LQ_IN_BOUNDS" in read(h)]
+            if "LQ_IN_BOUNDS" in text or shared:
+                flags |= set(re.findall(r"^LQ_DEBUG_FLAG_TAKE\((\w+)\)", text, re.M)) or {"none in " + f}
+    for name in flags:
+        assert f"lq::{name}()" in read("lq_api.cu") and f"unsigned {name}();" in read("lq_internal.h"), name
