@@ -36,6 +36,7 @@ SYMBOLS = ("lq_status_str", "lq_lifted_dim", "lq_pack_signs", "lq_unpack_signs",
            "lq_lift_activations_kron", "lq_gemv_workspace_size", "lq_gemv", "lq_gemv_noalloc", "lq_lift_gemv",
            "lq_gemm", "lq_gemm_epilogue", "lq_gemm_epilogue_workspace_size", "lq_gemv_epilogue",
            "lq_gemv_epilogue_workspace_size", "lq_gemm_grouped", "lq_gemm_grouped_workspace_size",
+           "lq_gemm_grouped_in_order_workspace_size",
            "lq_group_rows", "lq_combine_rows", "lq_encode", "lq_selftest_wait_timeout", "lq_selftest_bounds", "lq_is_debug_build",
            "lq_get_device_status")
 
@@ -84,7 +85,8 @@ def _load() -> ctypes.CDLL:
     lib.lq_encode.argtypes = [p, i, i, p, i, i, p, i, p, p]
     lib.lq_gemm.argtypes = [p, p, i, i, p, i, p, p]
     for name, argtypes in (("lq_gemm_epilogue_workspace_size", [i, i, i]), ("lq_gemv_epilogue_workspace_size", [i, i, i]),
-                           ("lq_gemm_grouped_workspace_size", [i, i, i, i])):
+                           ("lq_gemm_grouped_workspace_size", [i, i, i, i]),
+                           ("lq_gemm_grouped_in_order_workspace_size", [i, i, i, i])):
         getattr(lib, name).restype = z
         getattr(lib, name).argtypes = argtypes
     layer = [p, p, i, i, p, i, p, i, i, p, p, i, p, z, p]
@@ -399,9 +401,12 @@ def gemv_epilogue_workspace_size(out_rows: int, K: int, batch: int) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def gemm_grouped_workspace_size(experts: int, out_rows: int, K: int, n: int) -> int:
-    """Bytes of workspace gemm_grouped needs (0: refused sizes)."""
-    return 0 if not _fit(experts, out_rows, K, n) else int(lib.lq_gemm_grouped_workspace_size(experts, out_rows, K, n))
+def gemm_grouped_workspace_size(experts: int, out_rows: int, K: int, n: int, rows: bool = True) -> int:
+    """Bytes of workspace gemm_grouped needs, with or without `rows` (0: refused sizes)."""
+    if not _fit(experts, out_rows, K, n):
+        return 0
+    size = lib.lq_gemm_grouped_workspace_size if rows else lib.lq_gemm_grouped_in_order_workspace_size
+    return int(size(experts, out_rows, K, n))
 
 
 def _scratch(ws, need, like):
@@ -485,7 +490,7 @@ def gemm_grouped(packed, s, u, offsets, n, rows=None, bias=None, act=None, glu=F
     ot, o_t = _float_type(o_dtype if out is None else out.dtype)
     width = out_rows // 2 if glu else out_rows
     out, o = _result(out, "out", ot, (n, width), u)
-    ws, ws_bytes = _scratch(workspace, gemm_grouped_workspace_size(experts, out_rows, K, n), u)
+    ws, ws_bytes = _scratch(workspace, gemm_grouped_workspace_size(experts, out_rows, K, n, rows is not None), u)
     f32, i32 = torch.float32, torch.int32
     _check(lib.lq_gemm_grouped(_operand(packed, "packed", i32, (experts, out_rows, K // 32), dev),
                                _operand(s, "s", f32, (experts, out_rows), dev), experts, out_rows, K,

@@ -493,6 +493,16 @@ bool grouped_sizes_ok(int experts, int out, int K, int n) {
            count_ok((long long)experts * out);
 }
 
+// Workspace of a grouped call with or without rows.
+size_t grouped_need(int experts, int out, int K, int n, bool rows) {
+    if (!grouped_sizes_ok(experts, out, K, n)) return 0;
+    lq::GroupedCall c = sized_call(experts, out, K, n);
+    static const int some = 0;  // that there are offsets and rows counts, not where
+    c.offsets = &some;
+    c.rows = rows ? &some : nullptr;
+    return lq::grouped_workspace_size(c);
+}
+
 }  // namespace
 
 extern "C" {
@@ -531,12 +541,10 @@ int lq_gemv_epilogue(const uint32_t* packed, const float* s, int out, int K, con
                                               static_cast<cudaStream_t>(stream)));
 }
 
-size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n) {
-    if (!grouped_sizes_ok(experts, out, K, n)) return 0;
-    lq::GroupedCall c = sized_call(experts, out, K, n);
-    static const int some_offsets = 0;  // that there are offsets counts, not where
-    c.offsets = &some_offsets;
-    return lq::grouped_workspace_size(c);
+size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n) { return grouped_need(experts, out, K, n, true); }
+
+size_t lq_gemm_grouped_in_order_workspace_size(int experts, int out, int K, int n) {
+    return grouped_need(experts, out, K, n, false);
 }
 
 int lq_gemm_grouped(const uint32_t* packed, const float* s, int experts, int out, int K, const uint16_t* u_bf16,

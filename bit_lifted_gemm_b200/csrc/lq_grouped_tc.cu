@@ -577,7 +577,7 @@ size_t count_bytes(long long tiles) { return ((size_t)tiles * 16 + 255) / 256 * 
 }  // namespace
 
 size_t grouped_tc_workspace_size(const GroupedCall& c, int each) {
-    if (c.offsets) return (size_t)c.n * c.K * 2;  // used when rows are given
+    if (c.offsets) return c.rows ? (size_t)c.n * c.K * 2 : 0;  // the copied rows
     long long tiles;
     const int bn = tile_slots(each), parts = plan_split(c, bn, tiles);
     return parts > 1 ? count_bytes(tiles) + (size_t)tiles * parts * bn * BM * 4 : 0;

@@ -137,12 +137,12 @@ struct GroupedCall {
     void* o;               // [n][width], width = glu ? out / 2 : out
     bool o_bf16;
 };
-size_t grouped_workspace_size(const GroupedCall& c);  // sizes and types of c alone
+size_t grouped_workspace_size(const GroupedCall& c);  // sizes of c, and whether it has offsets and rows
 cudaError_t launch_grouped(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st);
 // Its kernel for few rows per expert (lq_grouped_mma.cu), on `sms` CTAs.
 cudaError_t launch_grouped_mma(const GroupedCall& c, unsigned* status, cudaStream_t st, int sms);
 // Its kernel for many rows per expert (lq_grouped_tc.cu): bf16 u, about `each` slots to an expert.
-size_t grouped_tc_workspace_size(const GroupedCall& c, int each);  // sizes of c, and whether it has offsets
+size_t grouped_tc_workspace_size(const GroupedCall& c, int each);  // sizes of c, and whether it has offsets and rows
 cudaError_t launch_grouped_tc(const GroupedCall& c, void* ws, unsigned* status, cudaStream_t st, int sms, int each);
 
 // Its path for a few slots, a slot at a time: the decode GEMV with the epilogue on u made fp32, a share of the

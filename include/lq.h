@@ -349,7 +349,8 @@ LQ_API size_t lq_gemv_epilogue_workspace_size(int out, int K, int batch);
  *   n       : slots, the extent of rows and o
  *   bias    : fp32 [experts][out] or NULL
  *   o       : [n][width], o_dtype; only slots of some expert are written
- *   workspace: lq_gemm_grouped_workspace_size(experts, out, K, n) bytes, as above
+ *   workspace: lq_gemm_grouped_workspace_size(experts, out, K, n) bytes, as above; with
+ *             rows NULL lq_gemm_grouped_in_order_workspace_size(...) are enough
  *   experts 1..4096, tokens >= 1, n >= 1; experts*out, K, tokens and n up to 2^31 - 4097
  * Kernels are chosen by n / min(n, experts), the slots of an expert if they spread
  * evenly; any sizes are right, very uneven ones slower. A slot's result does not
@@ -362,6 +363,9 @@ LQ_API int lq_gemm_grouped(const uint32_t* packed, const float* s, int experts, 
 
 /* Bytes of workspace lq_gemm_grouped needs; 0 for sizes it refuses. Host only. */
 LQ_API size_t lq_gemm_grouped_workspace_size(int experts, int out, int K, int n);
+
+/* The same for calls whose rows are NULL (no rows of u are gathered there). */
+LQ_API size_t lq_gemm_grouped_in_order_workspace_size(int experts, int out, int K, int n);
 
 /* Groups the (token, choice) pairs of a router by expert, for lq_gemm_grouped:
  *   expert_ids : int32 [tokens][topk]; ids outside 0..experts-1 are left out (a

@@ -263,3 +263,21 @@ def test_debug_build_checks_the_operators_kernels():
                 flags |= set(re.findall(r"^LQ_DEBUG_FLAG_TAKE\((\w+)\)", text, re.M)) or {"none in " + f}
     for name in flags:
         assert f"lq::{name}()" in read("lq_api.cu") and f"unsigned {name}();" in read("lq_internal.h"), name
+
+
+def test_grouped_workspace_without_rows(monkeypatch):
+    """Only rows are copied to the workspace of a product of many slots an expert; without them it needs next to nothing."""
+    import bit_lifted_gemm_b200 as lq
+    monkeypatch.setenv("LQ_FAULT", "launch")
+    for E, out, K, n in ((8, 4096, 10240, 8192), (3, 8, 64, 60), (5, 130, 1056, 70), (8, 11008, 10240, 2), (32, 2816, 4096, 128),
+                         (4, 256, 40960, 4)):
+        with_rows, without = lq.gemm_grouped_workspace_size(E, out, K, n), lq.gemm_grouped_workspace_size(E, out, K, n, rows=False)
+        assert 256 <= without <= with_rows
+        if n >= 9 * E:
+            assert without == 256 and with_rows == max(256, n * K * 2)
+        sizes = dict(experts=E, out=out, K=K, n=n, tokens=n)
+        for rows, need in ((far(3), with_rows), (None, without)):
+            assert call("lq_gemm_grouped", bytes=need, rows=rows, **sizes) == lq.LQ_ERR_CUDA
+            assert call("lq_gemm_grouped", bytes=need - 1, rows=rows, **sizes) == lq.LQ_ERR_INVALID_ARG
+    assert lq.gemm_grouped_workspace_size(4097, 8, 64, 1, rows=False) == 0
+    assert lq.gemm_grouped_workspace_size(4, 8, 64, OVER, rows=False) == 0
