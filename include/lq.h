@@ -304,8 +304,10 @@ typedef enum {
  *   o        : [tokens][width], o_dtype LQ_F32 or LQ_BF16 (written)
  *   workspace: 256-byte aligned device memory of at least
  *              lq_gemm_epilogue_workspace_size(out, K, tokens) bytes; its contents
- *              before the call do not matter. Calls that share one must be ordered. (Layers of
- *              few rows with many columns keep partial sums there, up to 57 MB.)
+ *              before the call do not matter. Calls that share one must be ordered.
+ *              (Layers of few tiles and many columns keep partial sums there, at most 58,199,552
+ *              bytes; layers of more than 18944 rows at 9 to 16 tokens take the bytes of
+ *              lq_gemv_epilogue and 4 K a token.)
  *   out >= 1, K >= 32, K % 32 == 0, tokens >= 1, none above 2^31 - 4097
  * Sums are exact or fp32 (one or two tokens, and wide layers at 9 to 16, take the
  * kernels of lq_gemv with their accuracy), and the result is rounded once, to o's

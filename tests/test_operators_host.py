@@ -281,3 +281,22 @@ def test_grouped_workspace_without_rows(monkeypatch):
             assert call("lq_gemm_grouped", bytes=need - 1, rows=rows, **sizes) == lq.LQ_ERR_INVALID_ARG
     assert lq.gemm_grouped_workspace_size(4097, 8, 64, 1, rows=False) == 0
     assert lq.gemm_grouped_workspace_size(4, 8, 64, OVER, rows=False) == 0
+
+
+def test_layer_workspace_stays_within_the_documented_bound():
+    """include/lq.h states the most that a layer's partial sums take: every number of tiles, at steps of K from few to many.
+    Nine to sixteen tokens of wide layers take the decode call's scratch beside u in fp32."""
+    import os
+    import re
+
+    import bit_lifted_gemm_b200 as lq
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "lq.h")) as f:
+        stated = [int(v.replace(",", "")) for v in re.findall(r"at most ([\d,]+)\s*\*?\s*bytes", f.read())]
+    assert len(stated) == 1
+    sizes = {(128 * blocks - 127 * ragged, K, tokens) for blocks in range(1, 300) for K in (64, 1056, 8192, 20480, 131072)
+             for tokens in (17, 64, 100, 256, 300, 512, 1000) for ragged in (0, 1)}
+    assert max(lq.gemm_epilogue_workspace_size(*size) for size in sizes) == stated[0]
+    for out, K, tokens in ((18945, 20480, 16), (28672, 4096, 9), (131072, 131072, 12)):
+        wide = 4 * K * tokens
+        assert wide % 256 == 0
+        assert lq.gemm_epilogue_workspace_size(out, K, tokens) == wide + lq.gemv_epilogue_workspace_size(out, K, tokens)
