@@ -282,7 +282,10 @@ LQ_API int lq_gemm(const uint32_t* packed, const float* s, int out, int K,
 
 /* Activations of the fused epilogues below, fp32 in and out:
  *   NONE z; RELU max(z, 0); GELU z/2 (1 + erf(z/sqrt 2));
- *   GELU_TANH z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); SILU z / (1 + e^-z). */
+ *   GELU_TANH z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); SILU z / (1 + e^-z).
+ * Accurate to a few fp32 steps relative to the value in the negative tails too (GELU: z^2
+ * steps), down to 10^-36. NaN stays NaN; -Inf gives NaN with GELU, GELU_TANH and SILU, as
+ * their formulas do in fp32. */
 typedef enum {
     LQ_ACT_NONE = 0,
     LQ_ACT_RELU = 1,

@@ -29,6 +29,33 @@ def activate(z, act):
     return z
 
 
+def activate_exact(z, act):
+    """(act(z), tol) of float64 values z that are exact in fp32, in forms that do not cancel where act is small, and what
+    evaluating act in fp32 may be off by:
+
+    gelu, z/2 erfc(x), x = -z/sqrt 2: the constant and its product are off by U32 each, which erfc turns into at most
+    2 U32 |x| (2/sqrt pi) e^(-x^2) / erfc(x) <= 2 U32 (1 + z^2) for z < 0, to U32 for
+    z >= 0; erfc itself is within 4 steps (8 U32), the last product U32.
+    gelu_tanh, z / (1 + e^(-2y)): y's two terms have one sign, so its seven roundings are off by 7 U32 |y|, 14 U32 |y| in
+    the exponential's argument; exp is within 2 steps (4 U32), and of both the share e/(1 + e) enters the sum (U32); the
+    quotient is within 2 steps (4 U32). silu: exp, sum and quotient, 9 U32. One more U32 each for products of these. none
+    and relu are exact.
+    A factor or denominator at the end of the normal range may be taken as 0: |z| 2^-126, and half the smallest step."""
+    with np.errstate(all="ignore"):
+        if act == "gelu":
+            o = 0.5 * z * np.vectorize(math.erfc, otypes=[np.float64])(-z / math.sqrt(2))
+            steps = np.where(z < 0, 2 * (1 + z * z), 1) + 10
+        elif act == "gelu_tanh":
+            y = math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+            share = 1 / (1 + np.exp(2 * y))
+            o, steps = z / (1 + np.exp(-2 * y)), (14 * np.abs(y) + 4) * share + 6
+        elif act == "silu":
+            o, steps = z / (1 + np.exp(-z)), 10.0
+        else:
+            return activate(z, act), np.zeros_like(z)
+        return o, np.abs(o) * steps * U32 + np.abs(z) * 2.0 ** -126 + 2.0 ** -150
+
+
 def layer(packed, s, u, bias=None, act=None, glu=False, residual=None):
     """(o, tol): o in float64, and the largest error an fp32 computation may make before its result is rounded.
 

@@ -657,3 +657,53 @@ def test_two_threads_at_once(lq):
     for t in threads:
         t.join()
     assert not wrong
+
+
+# tokens and type of u: the decode GEMV (fp32, and bf16 made fp32), its tcgen05 form, the mma.sync kernel, the tcgen05
+# kernel, and the same cut along K
+EPILOGUES = [(2, "f32", 64), (2, "bf16", 64), (16, "f32", 64), (5, "bf16", 64), (40, "bf16", 64), (300, "bf16", 64), (40, "bf16", 8192)]
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("tokens,u_t,K", EPILOGUES)
+def test_activations_are_accurate_in_their_tails(lq, act, glu, tokens, u_t, K):
+    """u = 0, so z is the bias exactly and the bound is the activation's own: down to where its value leaves fp32's
+    normal range, at both ends of that range, and among the smallest numbers."""
+    out = 1024
+    z = np.linspace(-120, 120, out).astype(np.float32)
+    z[:8] = [0.0, -0.0, 1e-30, -1e-30, 1e-40, -1e-40, 3e30, -3e30]
+    if glu:  # gates in the even rows, factors around 1 in the odd ones
+        bias = np.stack([z, np.linspace(-2, 2, out).astype(np.float32)], 1).reshape(-1)
+    else:
+        bias = z
+    rng = np.random.default_rng(28)
+    packed, s = make_layer(rng, (), bias.size, K)
+    call = lq.gemv_epilogue if u_t == "f32" else lq.gemm_epilogue
+    got = f64(call(dev(packed), gpu(s), gpu(np.zeros((tokens, K)), u_t == "bf16"), bias=gpu(bias), act=act, glu=glu))
+    want, tol = plain.activate_exact(z.astype(np.float64), act)
+    big = np.abs(z) > 1e30  # the bound's floor grows with |z|; the values are z and 0
+    tol[big] = 2 * plain.U32 * np.abs(want[big])
+    if glu:
+        other = bias[1::2].astype(np.float64)
+        want, tol = want * other, tol * np.abs(other) + 2.0 ** -150
+    assert got.shape == (tokens, out)
+    plain.assert_close(got, np.tile(want, (tokens, 1)), np.tile(tol, (tokens, 1)), False)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("glu", [False, True])
+@pytest.mark.parametrize("tokens,u_t,K", EPILOGUES)
+def test_activations_of_nan_and_inf(lq, act, glu, tokens, u_t, K):
+    bias = np.full(256, 0.5, np.float32)
+    step = 2 if glu else 1
+    bias[20], bias[40], bias[60] = np.nan, np.inf, -np.inf
+    rng = np.random.default_rng(29)
+    packed, s = make_layer(rng, (), bias.size, K)
+    call = lq.gemv_epilogue if u_t == "f32" else lq.gemm_epilogue
+    got = f64(call(dev(packed), gpu(s), gpu(np.zeros((tokens, K)), u_t == "bf16"), bias=gpu(bias), act=act, glu=glu))
+    low = {"none": -np.inf, "relu": 0.0}.get(act, np.nan)
+    for at, want in ((20, np.nan), (40, np.inf), (60, low)):
+        assert np.array_equal(got[:, at // step], np.full(tokens, want), equal_nan=True)
+    rest = np.delete(got, [20 // step, 40 // step, 60 // step], axis=1)
+    assert np.isfinite(rest).all() and (rest == rest[0, 0]).all()

@@ -300,3 +300,34 @@ def test_layer_workspace_stays_within_the_documented_bound():
         wide = 4 * K * tokens
         assert wide % 256 == 0
         assert lq.gemm_epilogue_workspace_size(out, K, tokens) == wide + lq.gemv_epilogue_workspace_size(out, K, tokens)
+
+
+def _misses(got, z, act):
+    want, tol = plain.activate_exact(z, act)
+    return int((np.abs(got.astype(np.float64) - want) > tol + plain.U32 * np.abs(want)).sum())
+
+
+def test_the_activations_bound_tells_forms_that_lose_the_tails():
+    """The bound that the kernels' activations are held to lets fp32 evaluations of the exact forms pass and none that cancel
+    or drop a tail."""
+    import math
+    f = np.float32
+    z = np.linspace(-60, 60, 4001).astype(f)
+    z64, tail = z.astype(np.float64), z < -3
+    erf, erfc = (np.vectorize(v, otypes=[np.float64]) for v in (math.erf, math.erfc))
+    x = f(0.70710678118654752) * z
+    y = f(0.79788456080286536) * (z + f(0.044715) * z * z * z)
+    with np.errstate(all="ignore"):
+        assert _misses(f(0.5) * z * erfc(-x).astype(f), z64, "gelu") == 0
+        assert _misses(z / (f(1) + np.exp(f(-2) * y)), z64, "gelu_tanh") == 0
+        assert _misses(z / (f(1) + np.exp(-z)), z64, "silu") == 0
+        assert _misses(f(0.5) * z * (f(1) + erf(x).astype(f)), z64, "gelu") > 100
+        assert _misses(f(0.5) * z * (f(1) + np.tanh(y)), z64, "gelu_tanh") > 100
+        for act, good in (("gelu", f(0.5) * z * erfc(-x).astype(f)), ("gelu_tanh", z / (f(1) + np.exp(f(-2) * y))),
+                          ("silu", z / (f(1) + np.exp(-z)))):
+            assert _misses(np.where(tail, f(0), good), z64, act) > 100
+            assert _misses(good * f(1 + 2e-4), z64, act) > 1000
+    # where float64 does not cancel both references are one
+    near = np.abs(z64) < 3
+    for act in ("gelu", "gelu_tanh", "silu", "relu", "none"):
+        assert np.allclose(plain.activate_exact(z64, act)[0][near], plain.activate(z64, act)[near], rtol=1e-12, atol=0)
