@@ -707,3 +707,35 @@ def test_activations_of_nan_and_inf(lq, act, glu, tokens, u_t, K):
         assert np.array_equal(got[:, at // step], np.full(tokens, want), equal_nan=True)
     rest = np.delete(got, [20 // step, 40 // step, 60 // step], axis=1)
     assert np.isfinite(rest).all() and (rest == rest[0, 0]).all()
+
+
+@pytest.mark.parametrize("E,n", [(12, 60), (5, 90), (40, 30)])  # five slots an expert, eighteen, and one
+@pytest.mark.parametrize("K", [96, 1056, 1152, 2048])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_rows_outside_read_nothing(lq, E, n, K, gather):
+    """Rows outside u count as zero rows, whatever lies beside u in memory (NaN here); offsets outside 0..n are cut;
+    slots of no expert keep their contents. At the sizes of each kernel, rows of words aligned and not."""
+    import torch
+    rng = np.random.default_rng([30, E, K])
+    out, tokens = 134, 20 if gather else n
+    packed, s = make_layer(rng, (E,), out, K)
+    bias = rng.standard_normal((E, out)).astype(np.float32)
+    u = bf16(rng.standard_normal((tokens, K)))
+    beside = torch.full((tokens + 16, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    beside[8: 8 + tokens] = gpu(u, True)
+    rows = rng.integers(-8, tokens + 8, n).astype(np.int32) if gather else None
+    if gather:
+        rows[:4] = [2 ** 31 - 1, -2 ** 31, -1, tokens]
+    for last in (n - 7, n + 500):  # slots left over, and an offset past the end
+        offsets = np.sort(rng.integers(0, n - 7, E + 1)).astype(np.int32)
+        offsets[0], offsets[1], offsets[-1] = -3, 5, last
+        offsets[1:] = np.maximum.accumulate(offsets[1:])
+        for glu, o_t in ((False, "f32"), (True, "bf16")):
+            width = out // 2 if glu else out
+            o = torch.full((n, width), 7.5, device="cuda", dtype=torch.float32 if o_t == "f32" else torch.bfloat16)
+            lq.gemm_grouped(dev(packed), gpu(s), beside[8: 8 + tokens], ints(offsets), n, rows=None if rows is None else ints(rows),
+                            bias=gpu(bias), act="silu", glu=glu, out=o)
+            want, tol, written = plain.grouped(packed, s.astype(np.float64), u, offsets, n, rows, bias, "silu", glu)
+            got = f64(o)
+            assert (got[~written] == 7.5).all() and written.sum() >= n - 7
+            plain.assert_close(got[written], want[written], tol[written], o_t == "bf16")
