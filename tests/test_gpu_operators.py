@@ -739,3 +739,48 @@ def test_grouped_rows_outside_read_nothing(lq, E, n, K, gather):
             got = f64(o)
             assert (got[~written] == 7.5).all() and written.sum() >= n - 7
             plain.assert_close(got[written], want[written], tol[written], o_t == "bf16")
+
+
+def whitening(rng, channels, t):
+    return np.stack([np.linalg.qr(rng.standard_normal((t, t)))[0] for _ in range(channels // t)]).astype(np.float32)
+
+
+@pytest.mark.parametrize("tokens,topk,model,hidden,t_in,t_hidden", [(1, 2, 320, 200, 32, 8), (9, 2, 320, 200, None, 40),
+                                                                    (100, 3, 640, 640, 128, 128)])
+def test_experts_block_with_whitening_and_dropped_choices(lq, tokens, topk, model, hidden, t_in, t_hidden):
+    """Each layer's own T^{-1}; most choices dropped, so that most slots of the inner tensors are never written, in memory that
+    held NaN before. Tolerance as in test_experts_block."""
+    import torch
+
+    import oracle
+    rng = np.random.default_rng([32, tokens])
+    E = 6
+    mlp, parts = expert_mlp(lq, rng, E, model, hidden, 10, 24)
+    tinv = [None if t is None else whitening(rng, c, t) for c, t in ((model, t_in), (hidden, t_hidden))]
+    mlp = type(mlp)(mlp.gate_up, mlp.gate_up_s, mlp.down, mlp.down_s, mlp.M, *(None if t is None else gpu(t) for t in tinv))
+    x = bf16(rng.standard_normal((tokens, model)))
+    ids = np.argsort(rng.random((tokens, E)), axis=1)[:, :topk].astype(np.int32)
+    ids[rng.random(ids.shape) < 0.6] = -1
+    ids[0, 0] = 3
+    w = rng.uniform(0.1, 1, (tokens, topk)).astype(np.float32)
+    gate, gs, up, us, down, ds, M = (np.asarray(p) for p in parts)
+
+    def lifted(a, t, K):
+        return bf16(lift(oracle.whiten(a, t), M.astype(np.float64), K)).astype(np.float64)
+
+    u = lifted(x.astype(np.float64), tinv[0], gate.shape[2] * 32)
+    want = x.astype(np.float64)
+    for i, j in np.argwhere(ids >= 0):
+        e = ids[i, j]
+        g, v = gs[e] * (plain.signs(gate[e]) @ u[i]), us[e] * (plain.signs(up[e]) @ u[i])
+        h = bf16(plain.activate(g, "silu") * v).astype(np.float64)
+        want[i] += float(w[i, j]) * bf16(ds[e] * (plain.signs(down[e]) @ lifted(h[None], tinv[1], down.shape[2] * 32)[0]))
+    args = gpu(x, True), ints(ids), gpu(w)
+    torch.cuda.synchronize()
+    poison = [torch.full((1 << b,), float("nan"), device="cuda") for b in range(6, 23)]
+    del poison
+    got = f64(mlp.step(*args))
+    added = np.abs(want - x).max(1, keepdims=True)
+    assert (np.abs(got - want) <= plain.UBF * np.abs(want) + 3 * 2.0 ** -7 * added).all()
+    none = (ids < 0).all(1)
+    assert np.array_equal(got[none], x[none].astype(np.float64))
