@@ -201,7 +201,8 @@ LQ_API size_t lq_gemv_workspace_size(int out, int K, int batch);
  * tcgen05 block-scaled 4-bit MMAs, which read every weight once for all
  * columns: u is converted once per call into the workspace, each 32-element
  * block with its own power-of-two scale to 21 bits (7 base-8 digits, error at
- * most 2^-21 of the block's largest |u|), accumulated in fp32 (~1e-6 relative).
+ * most 2^-21 of the power of two above the block's largest |u|), accumulated in
+ * fp32 (~1e-6 relative).
  * Non-finite activations propagate as in an exact IEEE sum: a column holding
  * a NaN gives NaN; a column holding +-Inf gives, per row, +-Inf or NaN by the
  * signs of its Inf terms.
@@ -312,9 +313,11 @@ typedef enum {
  *              bytes; layers of more than 18944 rows at 9 to 16 tokens take the bytes of
  *              lq_gemv_epilogue and 4 K a token.)
  *   out >= 1, K >= 32, K % 32 == 0, tokens >= 1, none above 2^31 - 4097
- * Sums are exact or fp32 (one or two tokens, and wide layers at 9 to 16, take the
- * kernels of lq_gemv with their accuracy), and the result is rounded once, to o's
- * type. A NaN or Inf in a row of u reaches that row of o alone, as in lq_gemv. Every
+ * Products are exact and their sums fp32, but for one or two tokens, and 9 to 16 of a
+ * layer of more than 18944 rows, which take the kernels of lq_gemv: exact sums of u
+ * held to 2^-31 of its row's largest |u|, and sums of u held to 2^-21 of the power of two
+ * above the largest of its 32 elements. So a token's last bits can depend on the number of
+ * tokens of its call. The result is rounded once, to o's type. A NaN or Inf in a row of u reaches that row of o alone, as in lq_gemv. Every
  * pointer must be memory of the current device. In place is refused (residual and o
  * may not overlap). Bounded waits report LQ_ERR_TIMEOUT through
  * lq_get_device_status. Requires an sm_100 device (else LQ_ERR_UNSUPPORTED). */

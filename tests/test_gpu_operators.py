@@ -741,6 +741,26 @@ def test_grouped_rows_outside_read_nothing(lq, E, n, K, gather):
             plain.assert_close(got[written], want[written], tol[written], o_t == "bf16")
 
 
+@pytest.mark.parametrize("tokens", [9, 12, 16])
+@pytest.mark.parametrize("K", [1056, 12288])
+def test_wide_layers_hold_bf16_rows_to_21_bits(lq, tokens, K):
+    """Layers of more than 18944 rows at 9 to 16 tokens: u may be off by 2^(E - 21), 2^E the power of two above the largest of
+    its 32 elements, whatever the spread among them (here up to 2^24), and no more; all other sums as elsewhere."""
+    out = 18945
+    rng = np.random.default_rng([31, tokens, K])
+    packed, s = make_layer(rng, (), out, K)
+    u = bf16(rng.standard_normal((tokens, K)) * 2.0 ** rng.integers(-24, 1, (tokens, K)))
+    rows = np.sort(rng.choice(out, 1500, replace=False))
+    rows[0], rows[-1] = 0, out - 1
+    want, tol = plain.layer(packed[rows], s[rows].astype(np.float64), u)
+    largest = np.abs(u.astype(np.float64)).reshape(tokens, -1, 32).max(2)
+    above = 2.0 ** (np.floor(np.log2(largest)) + 1)
+    tol = tol + s[rows] * (32 * above * 2.0 ** -21).sum(1)[:, None]
+    args = dev(packed), gpu(s), gpu(u, True)
+    assert lq.gemm_epilogue_workspace_size(out, K, tokens) > lq.gemv_epilogue_workspace_size(out, K, tokens)  # that route
+    plain.assert_close(f64(lq.gemm_epilogue(*args))[:, rows], want, tol, False)
+
+
 def whitening(rng, channels, t):
     return np.stack([np.linalg.qr(rng.standard_normal((t, t)))[0] for _ in range(channels // t)]).astype(np.float32)
 
