@@ -7,7 +7,7 @@
 // power-of-two scale, u_q[c][k] = round(u[c][k] * 2^F_c), |u_q| <= 2^30, held
 // as four balanced int8 digit planes u_q = d0 + 2^8 d1 + 2^16 d2 + 2^24 d3 (the
 // bytes of (u_q + 0x80808080) ^ 0x80808080). An element's rounding error is at
-// most 2^-31 of the largest |u| of its column and K range. The kernel adds the
+// most 2^-31 of the power of two above the largest |u| of its column and K range. The kernel adds the
 // digits of the set bits exactly in integers (sum sigma u_q = 2 sum_{bit=1} u_q
 // - sum u_q), so the only rounding is this quantization and the final stores.
 // Columns holding a NaN are written as NaN; columns holding +-Inf are

@@ -22,9 +22,11 @@
 //
 // What bounds it. Wide tiles: the tensor cores under the power cap (13824 x 12288, 2048 tokens, gated:
 // 427 us = 1630 TFLOP/s in short bursts, 499 us = 1394 of the 1434 TFLOP/s that the library's product
-// sustains). Narrow ones: shared memory, since every sign becomes two bytes that are written and read
-// there: 64 rows by 128 k take 32 + 32 KB for the signs and 16 + 16 KB for u, 768 clocks at 128 bytes
-// each, of the 740 measured (64 tokens 38 us, 128 tokens 56 us).
+// sustains). Narrow ones: no unit is saturated. Of a CTA's active time at 64 tokens the tensor pipe works 31%, the ALU
+// pipe (the expansion) 53%, and both sides of shared memory run at less than the rates that wide tiles reach (the
+// stores of signs and u 58 against 70%, the MMAs' reads 46 against 65%); a step of 128 k takes 740 clocks, which are
+// waits of the roles for one another and for sign words on their way (38 us warm, 44 with the signs from HBM; 128
+// tokens 54 and 58). And 108 tiles leave a quarter of the SMs idle. Which of the waits is the longest is not known.
 #include <cuda.h>
 
 #include "lq_debug.cuh"

@@ -194,8 +194,8 @@ LQ_API size_t lq_gemv_workspace_size(int out, int K, int batch);
  * Arithmetic: one or two columns (three below 40 MB of packed weights) run on
  * mma.sync, which converts each
  * column of u (over the K range of each launch) to 32-bit fixed point with one
- * power-of-two scale -- an element's error is at most 2^-31 of the largest |u|
- * of its column and range -- and contracts the signs in exact integer
+ * power-of-two scale -- an element's error is at most 2^-31 of the power of two
+ * above the largest |u| of its column and range -- and contracts the signs in exact integer
  * arithmetic; the result is within ~1e-7 relative (Frobenius) of the exact
  * value, and equal to it when u holds small integers. More columns run on
  * tcgen05 block-scaled 4-bit MMAs, which read every weight once for all
@@ -314,9 +314,9 @@ typedef enum {
  *              lq_gemv_epilogue and 4 K a token.)
  *   out >= 1, K >= 32, K % 32 == 0, tokens >= 1, none above 2^31 - 4097
  * Products are exact and their sums fp32, but for one or two tokens, and 9 to 16 of a
- * layer of more than 18944 rows, which take the kernels of lq_gemv: exact sums of u
- * held to 2^-31 of its row's largest |u|, and sums of u held to 2^-21 of the power of two
- * above the largest of its 32 elements. So a token's last bits can depend on the number of
+ * layer of more than 18944 rows, which take the kernels of lq_gemv: exact sums of u held
+ * to 2^-31 of the power of two above its row's largest, and fp32 sums of u held to 2^-21
+ * of the power of two above the largest of its 32 elements. So a token's last bits can depend on the number of
  * tokens of its call. The result is rounded once, to o's type. A NaN or Inf in a row of u reaches that row of o alone, as in lq_gemv. Every
  * pointer must be memory of the current device. In place is refused (residual and o
  * may not overlap). Bounded waits report LQ_ERR_TIMEOUT through
