@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 // A thread owns 16 bytes of a token's row (one element where rows are not 16-byte
 // aligned) and adds the token's slots in order, the loads of four issued together. Bound by
 // reading the y rows and writing o: 4096 tokens of four slots of 4096 bf16 37.5 us, 5.4 TB/s (83% of the measured copy).
+// An element a thread takes 129 us for a width of 4095 (1.6 TB/s in loads of two bytes).
 template <bool BF16, int N>
 struct Chunk {
     typename Elem<BF16>::T v[N];
